@@ -21,6 +21,8 @@
  *    Query head h reads KV head h / (Hq / Hkv). Head dimension d is 64 or 128.
  *  - Every call is asynchronous and stream-ordered on `stream` (a cudaStream_t; NULL is the
  *    legacy default stream). Nothing synchronises except sep_last_device_error().
+ *  - The calls with a dtype argument (sep_rope_*, seppaged_*) take element strides where they are
+ *    listed, in place of contiguity.
  *  - Return value: SEP_OK, or an error code below; on an argument error nothing is launched.
  *    Device-side failures (a bounded wait that ran out) set a sticky device error word that
  *    sep_last_device_error() reads and clears.
@@ -46,8 +48,13 @@ enum {
   SEP_ERR_CUDA = 4,          /* a CUDA runtime/driver call or a launch failed */
   SEP_ERR_TIMEOUT = 5,       /* device: a bounded pipeline wait ran out (reported sticky) */
   SEP_ERR_WORKSPACE = 6,     /* workspace pointer null or smaller than the size query says */
-  SEP_ERR_SCRATCH_LIMIT = 7  /* sep_attn_fwd_noalloc: problem larger than its fixed scratch */
+  SEP_ERR_SCRATCH_LIMIT = 7, /* sep_attn_fwd_noalloc: problem larger than its fixed scratch */
+  SEP_ERR_INDEX = 8          /* device: a page table, length or offset array held a value out of
+                                range (reported sticky; the entry was skipped) */
 };
+
+/* Element types of the rotary and paged-cache calls. */
+enum { SEP_DTYPE_BF16 = 0, SEP_DTYPE_F16 = 1, SEP_DTYPE_F32 = 2 };
 
 /* Tile sizes the attention kernels use: query tiles of 128 rows, key tiles of 128 columns. */
 #define SEP_TILE_M 128
@@ -304,6 +311,116 @@ const char* sep_status_string(int status);
 int sep_attn_fwd_noalloc(const sep_bf16* q, const sep_bf16* k, const sep_bf16* v,
                          int B, int L, int Hq, int Hkv, int d, float scale, int a, int n,
                          const SepMask* mask, sep_bf16* o, float* lse, sep_stream_t stream);
+
+/*
+ * sep_rope_fwd / sep_rope_bwd - rotary positions on queries and keys (one kernel for both).
+ *
+ * Pair z (0 <= z < d_rot / 2) of each head at position p turns by p * freq[z]: with (c, s) =
+ * magnitude * (cos, sin) of that angle, y1 = x1 c - x2 s, y2 = x2 c + x1 s. The pair is elements
+ * (z, z + d_rot / 2), or (2z, 2z + 1) when interleaved; elements from d_rot on are copied.
+ * Angles are formed in fp64, the rotation in fp32, each result is rounded once. sep_rope_bwd maps
+ * gradients of the outputs to gradients of the inputs (the angle negated, the magnitude kept).
+ * This is the rotation in front of sep_attn_fwd, sepcache_decode without shifting
+ * (original_positions) and seppaged_attn; SepCache and seppaged_append rotate keys themselves.
+ *
+ * Tensors are [B, L, H, d] with element strides for batch, token and head and contiguous heads
+ * (views of a fused projection will do). y may equal x with the same strides (in place: elements
+ * from d_rot on are then not touched); other overlaps are not allowed. k may be NULL. Any
+ * element-aligned address works; 16-byte aligned rows and halves take 16-byte accesses.
+ * pos: int32 (pos64 = 0) or int64 [L] per batch, batch b's at pos + b * pos_stride (0: shared).
+ * dtype BF16, F16 or F32. 2 <= d_rot <= d <= 512, d_rot even; B * L <= 2^31 - 1.
+ */
+typedef struct SepRope {
+  const double* freq;  /* [d_rot / 2] angle per position step of each pair (device) */
+  int32_t d_rot;       /* rotated elements of a head, even */
+  int32_t interleaved; /* pairs (2z, 2z + 1) instead of (z, z + d_rot / 2) */
+  float magnitude;     /* factor of cos and sin (1 unless the frequency scaling has one) */
+} SepRope;
+typedef struct SepRopeTensor {
+  const void* x;
+  void* y;
+  int64_t x_stride[3], y_stride[3]; /* elements: batch, token, head */
+  int32_t H;
+} SepRopeTensor;
+int sep_rope_fwd(const SepRope* rope, int dtype, int B, int L, int d, const void* pos, int pos64,
+                 int64_t pos_stride, const SepRopeTensor* q, const SepRopeTensor* k,
+                 sep_stream_t stream);
+int sep_rope_bwd(const SepRope* rope, int dtype, int B, int L, int d, const void* pos, int pos64,
+                 int64_t pos_stride, const SepRopeTensor* dq, const SepRopeTensor* dk,
+                 sep_stream_t stream);
+
+/*
+ * Paged cache: keys and values of many sequences in pages of e4m3 numbers, every token kept (the
+ * counterpart of SepCache for layers that keep the whole history, dense or under the separator
+ * rule). Page p holds `page` consecutive tokens of one sequence; sequence s, position j lives in
+ * page table[s][j / page], slot j % page. For each (page, KV head) K and V have one scale, a power
+ * of two 2^e with the smallest e >= -100 such that every finite value of the page's rows is at
+ * most 448 * 2^e, or 0 while all of them are 0: value = scale * stored number. The scale of a page
+ * starts with its slot 0 and grows with later rows (rows held are then re-expressed: exact, but
+ * for numbers that fall into e4m3's subnormals, which are rounded again). Values that are not
+ * finite are stored as NaN.
+ *
+ * All memory is the caller's and needs no initialisation: a page is read only up to its
+ * sequence's length. Sizes in elements:
+ *   k_pages, v_pages  num_pages * Hkv * page * d  e4m3    16-byte aligned
+ *   k_scale, v_scale  num_pages * Hkv             fp32
+ *   flags             num_pages * page            uint8   separator flag of each slot, 16-byte aligned
+ * d is 64 or 128; page is 16, 32, 64 or 128; num_pages * Hkv * page < 2^32.
+ * rope: the rotation of appended keys at their positions (rope.d_rot = 0: keys are stored as given).
+ */
+typedef struct SepPagedState {
+  int32_t num_pages, Hkv, d, page;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  float* k_scale;
+  float* v_scale;
+  uint8_t* flags;
+  SepRope rope;
+} SepPagedState;
+
+/*
+ * Index arrays of seppaged_append and seppaged_attn, on the device, read when the kernels run (a
+ * captured graph sees their values at each replay):
+ *   page_table [S, max_pages] int32  entries past a sequence's pages are not read
+ *   seq_lens   [S] int32             tokens of each sequence INCLUDING the call's new ones (< 2^30)
+ *   indptr     [S + 1] int32         tokens indptr[s] .. indptr[s + 1] - 1 of the call are the newest
+ *                                    of sequence s, in order; ascending, within 0 .. T
+ * Token i of the c tokens of sequence s stands at position seq_lens[s] - c + i. Tokens before
+ * indptr[0] and from indptr[S] on, and tokens with a negative position, are padding: not
+ * appended; the outputs of the former are left as they were, the latter get o = 0, lse = -inf.
+ * A value out of range (a page number, a length beyond max_pages * page, an offset) is skipped and
+ * reported as SEP_ERR_INDEX by sep_last_device_error().
+ *
+ * seppaged_append - store the new tokens' keys and values (one kernel).
+ * k, v [T, Hkv, d] bf16 or fp16 (dtype), element strides for token and head, multiples of 8; sep [T]
+ * uint8 (NULL: no separators). A page that a call writes belongs to one sequence of the call
+ * (shared prefixes are shared as whole pages in front of it).
+ */
+int seppaged_append(const SepPagedState* st, int dtype, const void* k, int64_t k_token_stride,
+                    int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                    int64_t v_head_stride, const uint8_t* sep, int T, int S, int max_pages,
+                    const int32_t* page_table, const int32_t* seq_lens, const int32_t* indptr,
+                    sep_stream_t stream);
+
+/*
+ * seppaged_attn - attention of the newest tokens of each sequence over its pages.
+ * The query at position p keeps key j iff j <= p && (p - j < n || j < a || flag[j]), the rule of
+ * sep_mask_build (n = INT32_MAX: every key up to p; n = 0: only initial tokens and separators).
+ * O = softmax(scale * q . k over kept j) V, lse = ln sum exp (fp32); a query that keeps nothing
+ * gets o = 0, lse = -inf. One token per sequence (decode), several (drafted tokens) or many (a
+ * prompt's chunk); the tokens' own keys must have been appended.
+ * q [T, Hq, d] bf16 or fp16, already rotated, element strides for token and head, multiples of 8;
+ * o [T, Hq, d] contiguous, of q's type; lse [T, Hq] fp32 (NULL: not written). Hq % Hkv == 0,
+ * S <= 4096, T * Hq < 2^31, a >= 0, n >= 0. workspace: 256-byte aligned, of
+ * seppaged_attn_workspace_size(S, d) bytes, needs no initialisation and carries nothing from one
+ * call to the next; calls that may overlap in time (graphs on two streams) need one each.
+ */
+size_t seppaged_attn_workspace_size(int S, int d);
+int seppaged_attn(const SepPagedState* st, int dtype, const void* q, int64_t q_token_stride,
+                  int64_t q_head_stride, int Hq, int T, int S, int max_pages,
+                  const int32_t* page_table, const int32_t* seq_lens, const int32_t* indptr, int a,
+                  int n, float scale, void* o, float* lse, void* workspace,
+                  size_t workspace_bytes, sep_stream_t stream);
 
 #ifdef __cplusplus
 }

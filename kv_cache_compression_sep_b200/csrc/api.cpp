@@ -301,6 +301,107 @@ int sepcache_export_order(const SepCacheState* st, int32_t* pos_out, int32_t* co
       sep::launch_sepcache_export(*st, pos_out, count, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static int check_rope(const SepRope& r, int d) {
+  if (!r.freq) return SEP_ERR_INVALID_ARG;
+  if (r.d_rot < 2 || r.d_rot > d || r.d_rot % 2 != 0) return SEP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(r.freq) & 7u) != 0) return SEP_ERR_MISALIGNED;
+  return SEP_OK;
+}
+
+static int rope_impl(const SepRope* rope, int dtype, int B, int L, int d, const void* pos,
+                     int pos64, int64_t pos_stride, const SepRopeTensor* q, const SepRopeTensor* k,
+                     float sign, sep_stream_t stream) {
+  if (!rope || !pos || !q || B < 1 || L < 1 || d < 2) return SEP_ERR_INVALID_ARG;
+  if ((long long)B * L > 2147483647ll) return SEP_ERR_UNSUPPORTED;
+  if (d > 512 || dtype < SEP_DTYPE_BF16 || dtype > SEP_DTYPE_F32) return SEP_ERR_UNSUPPORTED;
+  const int e = check_rope(*rope, d);
+  if (e != SEP_OK) return e;
+  const uintptr_t es = dtype == SEP_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(pos) % (pos64 ? 8 : 4) != 0) return SEP_ERR_MISALIGNED;
+  for (const SepRopeTensor* t : {q, k}) {
+    if (!t) continue;
+    if (!t->x || !t->y || t->H < 1 || t->H > 65536) return SEP_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(t->x) % es != 0 || reinterpret_cast<uintptr_t>(t->y) % es != 0)
+      return SEP_ERR_MISALIGNED;
+  }
+  return cuda_status(sep::launch_rope(*rope, dtype, B, L, d, pos, pos64, pos_stride, q, k, sign,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int sep_rope_fwd(const SepRope* rope, int dtype, int B, int L, int d, const void* pos, int pos64,
+                 int64_t pos_stride, const SepRopeTensor* q, const SepRopeTensor* k,
+                 sep_stream_t stream) {
+  return rope_impl(rope, dtype, B, L, d, pos, pos64, pos_stride, q, k, 1.f, stream);
+}
+
+int sep_rope_bwd(const SepRope* rope, int dtype, int B, int L, int d, const void* pos, int pos64,
+                 int64_t pos_stride, const SepRopeTensor* dq, const SepRopeTensor* dk,
+                 sep_stream_t stream) {
+  return rope_impl(rope, dtype, B, L, d, pos, pos64, pos_stride, dq, dk, -1.f, stream);
+}
+
+static int check_paged(const SepPagedState* st, int dtype, int T, int S, int max_pages,
+                       const int32_t* page_table, const int32_t* seq_lens, const int32_t* indptr) {
+  if (!st || !page_table || !seq_lens || !indptr) return SEP_ERR_INVALID_ARG;
+  if (!st->k_pages || !st->v_pages || !st->k_scale || !st->v_scale || !st->flags)
+    return SEP_ERR_INVALID_ARG;
+  if (st->num_pages < 1 || st->Hkv < 1 || T < 1 || S < 1 || max_pages < 1)
+    return SEP_ERR_INVALID_ARG;
+  if (st->d != 64 && st->d != 128) return SEP_ERR_UNSUPPORTED;
+  if (st->page != 16 && st->page != 32 && st->page != 64 && st->page != 128)
+    return SEP_ERR_UNSUPPORTED;
+  if (dtype != SEP_DTYPE_BF16 && dtype != SEP_DTYPE_F16) return SEP_ERR_UNSUPPORTED;
+  // rows of the pools are numbered in 32 bits
+  if ((unsigned long long)st->num_pages * st->Hkv >= (1ull << 32) / st->page)
+    return SEP_ERR_UNSUPPORTED;
+  if (!aligned16(st->k_pages) || !aligned16(st->v_pages) || !aligned16(st->flags))
+    return SEP_ERR_MISALIGNED;
+  return SEP_OK;
+}
+
+int seppaged_append(const SepPagedState* st, int dtype, const void* k, int64_t k_token_stride,
+                    int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                    int64_t v_head_stride, const uint8_t* sep, int T, int S, int max_pages,
+                    const int32_t* page_table, const int32_t* seq_lens, const int32_t* indptr,
+                    sep_stream_t stream) {
+  int e = check_paged(st, dtype, T, S, max_pages, page_table, seq_lens, indptr);
+  if (e != SEP_OK) return e;
+  if (!k || !v) return SEP_ERR_INVALID_ARG;
+  if (st->rope.d_rot != 0) {
+    e = check_rope(st->rope, st->d);
+    if (e != SEP_OK) return e;
+  }
+  if (!aligned16(k) || !aligned16(v) || k_token_stride % 8 != 0 || k_head_stride % 8 != 0 ||
+      v_token_stride % 8 != 0 || v_head_stride % 8 != 0)
+    return SEP_ERR_MISALIGNED;
+  return cuda_status(sep::launch_paged_append(
+      *st, dtype, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, sep, T, S,
+      max_pages, page_table, seq_lens, indptr, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t seppaged_attn_workspace_size(int S, int d) {
+  if (S < 1 || d < 1) return 0;
+  return sep::paged_attn_workspace(S, d);
+}
+
+int seppaged_attn(const SepPagedState* st, int dtype, const void* q, int64_t q_token_stride,
+                  int64_t q_head_stride, int Hq, int T, int S, int max_pages,
+                  const int32_t* page_table, const int32_t* seq_lens, const int32_t* indptr, int a,
+                  int n, float scale, void* o, float* lse, void* workspace,
+                  size_t workspace_bytes, sep_stream_t stream) {
+  int e = check_paged(st, dtype, T, S, max_pages, page_table, seq_lens, indptr);
+  if (e != SEP_OK) return e;
+  if (!q || !o || Hq < 1 || Hq % st->Hkv != 0 || a < 0 || n < 0) return SEP_ERR_INVALID_ARG;
+  if (S > 4096 || (long long)T * Hq > 2147483647ll) return SEP_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(o) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0)
+    return SEP_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < sep::paged_attn_workspace(S, st->d)) return SEP_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SEP_ERR_MISALIGNED;
+  return cuda_status(sep::launch_paged_attn(*st, dtype, q, q_token_stride, q_head_stride, Hq, T, S,
+                                            max_pages, page_table, seq_lens, indptr, a, n, scale, o,
+                                            lse, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int sep_last_device_error(void) {
   unsigned* p = sep::device_error_word();
   if (!p) return SEP_ERR_CUDA;
@@ -346,6 +447,7 @@ const char* sep_status_string(int status) {
     case SEP_ERR_WORKSPACE: return "workspace missing or too small";
     case SEP_ERR_SCRATCH_LIMIT:
       return "problem needs more than the fixed scratch of sep_attn_fwd_noalloc";
+    case SEP_ERR_INDEX: return "a page table, length or offset entry was out of range";
     default: return "unknown status";
   }
 }

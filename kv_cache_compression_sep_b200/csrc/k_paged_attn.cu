@@ -1,0 +1,909 @@
+// seppaged_attn: attention of the newest tokens of each sequence over its pages of e4m3 keys and
+// values (one power-of-two scale per page and KV head), under the separator keep rule.
+//
+// Query token i of a sequence with c queries and length len stands at p = len - c + i and keeps key j
+// iff j <= p and (p - j < n or j < a or flag[j]). With s_j = scale * ks_j * q . k_j and the value row
+// vs_j * v_j (k, v the stored e4m3 numbers), O = sum_j 2^(s'_j - M) vs_j v_j / sum_j 2^(s'_j - M),
+// s' = s log2 e. The weights of the values are carried as w_j = 2^(s'_j + log2 vs_j - Mo) with a
+// running maximum Mo of their own, so that pages with small and large value scales enter the same
+// fp16 product with full precision; the row sum has the usual running maximum M, and the two meet
+// in the last step: O = acc 2^(Mo - M) / l.
+//
+// The stored numbers are read once from HBM and that bounds the call (2 d bytes per key and KV
+// head, 4 d flops per query head). One warp is the unit of work: it takes 8 NT query rows (the
+// group's heads of one or more tokens) against a run of keys, its keys and values go from global
+// memory straight into the fragments of mma.sync (S^T = K Q^T and O^T = V^T P^T, keys or value
+// columns on the 16-row side, so that 8 query rows fill the 8-column side), and nothing in the
+// main loop waits for another warp. e4m3 -> fp16 is exact; queries enter as fp16 scaled per row
+// by a power of two (bf16 has fewer significant bits, so that is exact above 2^-28 of the row's
+// largest); the weights are rounded to fp16 (2^-11); sums are fp32. The tensor cores are far from
+// busy here (a query group of 8 rows uses 2 x 8 x 16 x 16 products per 16 keys and 16 columns), so
+// mma.sync fragments fed from registers are the better side than tcgen05, whose operands would
+// have to be converted through shared memory.
+//
+// Work split: every (sequence, KV head, row tile) has a number of key tiles, all tiles of the call
+// are numbered in a row, and each warp takes an equal run of them, wherever sequences begin and
+// end. A warp that covers all tiles of a row tile writes the result; otherwise it leaves its part
+// in the workspace and seppaged_join_kernel adds the parts in the order of the warps (same bits
+// every time).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "sep_common.cuh"
+#include "sep_launch.h"
+#include "sep_rope.cuh"
+
+namespace sep {
+
+namespace {
+
+constexpr int kWarps = 4;            // per CTA
+constexpr int kScan = 512;           // positions of a tile left of the window (kept rows are gathered)
+constexpr int kDense = 64;           // positions of a window tile (every row loaded)
+constexpr int kMaxWarps = 2048;      // workspace slots are laid out for this many
+
+struct PagedAttnParams {
+  const uint8_t *k_pages, *v_pages;
+  const float *k_scale, *v_scale;
+  const uint8_t* flags;
+  const void* q;
+  long long q_tok, q_head;
+  void* o;
+  float* lse;
+  const int32_t *table, *lens, *indptr;
+  long long* base;  // [S + 1] first tile of each sequence (workspace)
+  float* part;      // parts of row tiles that several warps share (workspace)
+  unsigned* err;
+  int T, S, Hq, Hkv, G, num_pages, max_pages, log_page, a, n, bf16, nwarps;
+  float scale_log2;
+};
+
+// ------------------------------------------------------------------ tiles of a sequence
+struct SeqInfo {
+  int len;       // tokens in the pages that may be read
+  int tok0, nq;  // first query token and count
+  int lead;      // position of query 0 (negative: padding queries, which keep nothing)
+  bool bad;      // an index was out of range
+};
+constexpr int kMaxLen = 1 << 30;
+__device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int s) {
+  SeqInfo q;
+  const int i0 = __ldg(p.indptr + s), i1 = __ldg(p.indptr + s + 1);
+  q.tok0 = max(0, min(i0, p.T));
+  q.nq = max(0, min(i1, p.T) - q.tok0);
+  const int len = __ldg(p.lens + s);
+  q.len = (int)min((long long)min(max(len, 0), kMaxLen), (long long)p.max_pages << p.log_page);
+  q.lead = q.len - q.nq;
+  q.bad = i0 != q.tok0 || i1 != q.tok0 + q.nq || len != q.len;
+  return q;
+}
+// Row tile rt covers rows rt * R .. of the sequence's nq * G (token, head in group) rows.
+struct RowTile {
+  int w0, kend;  // keys [w0, kend) are loaded whole, keys [0, w0) only where kept by every row
+  int ns, nd;    // scan tiles and window tiles
+};
+__device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, const SeqInfo& q, int rt, int R) {
+  RowTile r;
+  const int i_lo = rt * R / p.G, i_hi = min(q.nq - 1, (rt * R + R - 1) / p.G);
+  const int lo = max(q.lead + i_lo, 0), hi = q.lead + i_hi;
+  r.kend = max(0, hi + 1);
+  r.w0 = min(max(0, lo - max(p.n, 1) + 1), r.kend) & ~(kDense - 1);
+  r.ns = (r.w0 + kScan - 1) / kScan;
+  r.nd = (r.kend - r.w0 + kDense - 1) / kDense;
+  return r;
+}
+// Tiles numbered for each row tile of a sequence: the largest count that one of them can have.
+__device__ __forceinline__ int tiles_per_row_tile(const PagedAttnParams& p, const SeqInfo& q, int R) {
+  const int span = min(q.nq, R / p.G + 2);
+  const int all = (q.len + kDense - 1) / kDense;
+  const long long win = ((long long)p.n + span + 2 * kDense - 2) / kDense;
+  if (win >= all) return all;
+  const int last_w0 = max(0, q.len - max(p.n, 1) + 1);
+  return min(all, (int)win + (last_w0 + kScan - 1) / kScan);
+}
+__device__ __forceinline__ int row_tiles(const PagedAttnParams& p, const SeqInfo& q, int R) {
+  return (int)(((long long)q.nq * p.G + R - 1) / R);
+}
+
+// ------------------------------------------------------------------ fragments
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t w) {  // low 16 bits: two e4m3 -> two fp16
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_e4m3x2_hi(uint32_t w) {  // high 16 bits
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Byte masks of the NaN bytes (0x7f, 0xff) of four e4m3 values: 0x80 in each such byte.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+constexpr uint32_t kNoRow = 0xffffffffu;
+
+// log2 of a page's scale: a power of two, or 0 while the page holds only zeros
+__device__ __forceinline__ float log2_of_scale(float s) {
+  return s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : -INFINITY;
+}
+
+// Keys and values of 32 positions in fragment order. Lane (g = lane / 4, t = lane % 4):
+// K: key 16 i + 8 u + g, elements 16 t .. 16 t + 15 of each 64; V: keys 16 i + 2 t + {0, 1, 8, 9},
+// columns (D / 8) g ..
+template <int D>
+struct KFrag {
+  uint4 x[2][2][D / 64];
+};
+template <int D>
+struct VFrag {
+  uint32_t x[2][4][D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ void load_k(KFrag<D>& f, const uint8_t* base, const uint32_t (&row)[2][2], int t) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int z = 0; z < D / 64; ++z) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row[i][u] != kNoRow)
+          v = __ldg(reinterpret_cast<const uint4*>(base + (size_t)row[i][u] * D + z * 64 + t * 16));
+        f.x[i][u][z] = v;
+      }
+}
+template <int D>
+__device__ __forceinline__ void load_v(VFrag<D>& f, const uint8_t* base, const uint32_t (&row)[2][4], int g) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool on = row[i][u] != kNoRow;
+      const uint8_t* a = base + (size_t)row[i][u] * D + g * (D / 8);
+      if (D == 128) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (on) v = __ldg(reinterpret_cast<const uint4*>(a));
+        f.x[i][u][0] = v.x;
+        f.x[i][u][1] = v.y;
+        f.x[i][u][D / 32 - 2] = v.z;
+        f.x[i][u][D / 32 - 1] = v.w;
+      } else {
+        uint2 v = make_uint2(0u, 0u);
+        if (on) v = __ldg(reinterpret_cast<const uint2*>(a));
+        f.x[i][u][0] = v.x;
+        f.x[i][u][1] = v.y;
+      }
+    }
+}
+
+// Running state of one row tile in one warp. Lane (g, t) holds, for row tile part nt, rows 2 t and
+// 2 t + 1: accumulators of columns (D / 8) g + 2 mt + {0, 1}, and the statistics of both rows.
+template <int D, int NT>
+struct RowState {
+  float acc[NT][D / 16][4];
+  float m[NT][2], mo[NT][2], l[NT][2];  // l: this lane's keys only
+  uint32_t q[NT][D / 16][2];
+  float qs[NT][2];   // 2^-(row exponent) * scale * log2 e
+  int pos[NT][2];
+  bool live[NT][2];
+};
+
+// ------------------------------------------------------------------ 32 keys
+// ks, ve [i][u]: key scale and log2 of the value scale of key 16 i + 8 u + g. MASK: kpos (position, or
+// -1 for none) and anchor (kept whatever the distance) of the same keys decide row by row.
+template <int D, int NT, bool MASK>
+__device__ __forceinline__ void step32(const PagedAttnParams& p, RowState<D, NT>& r, const KFrag<D>& kf,
+                                       const VFrag<D>& vf, const float (&ks)[2][2], const float (&ve)[2][2],
+                                       const int (&kpos)[2][2], const bool (&anchor)[2][2]) {
+  // ---- S^T = K Q^T
+  float s[NT][2][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[nt][i][c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int z = 0; z < D / 64; ++z) {
+      const uint4 x = kf.x[i][0][z], y = kf.x[i][1][z];
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a0 = cvt_e4m3x2(xw[w]), a2 = cvt_e4m3x2_hi(xw[w]);
+        const uint32_t a1 = cvt_e4m3x2(yw[w]), a3 = cvt_e4m3x2_hi(yw[w]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816(s[nt][i], a0, a1, a2, a3, r.q[nt][z * 4 + w][0], r.q[nt][z * 4 + w][1]);
+      }
+    }
+  uint32_t pb[NT][2][2];
+  uint32_t keep = 0;  // MASK: bit nt * 8 + i * 4 + c
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float mx[2] = {-INFINITY, -INFINITY}, mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int u = c >> 1, e = c & 1;
+        float x = s[nt][i][c] * (ks[i][u] * r.qs[nt][e]);
+        if (MASK) {
+          const int dist = r.pos[nt][e] - kpos[i][u];
+          const bool on = r.live[nt][e] && kpos[i][u] >= 0 && dist >= 0 && (dist < p.n || anchor[i][u]);
+          if (!on) x = -INFINITY;
+          keep |= (on ? 1u : 0u) << (nt * 8 + i * 4 + c);
+        }
+        s[nt][i][c] = x;
+        mx[e] = fmaxf(mx[e], x);
+        mt[e] = fmaxf(mt[e], x + ve[i][u]);
+      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+        mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], o));
+      }
+      const float m_new = fmaxf(r.m[nt][e], mx[e]), mo_new = fmaxf(r.mo[nt][e], mt[e]);
+      const float m_ref = m_new == -INFINITY ? 0.f : m_new, mo_ref = mo_new == -INFINITY ? 0.f : mo_new;
+      r.l[nt][e] *= ex2(r.m[nt][e] - m_ref);
+      const float f = ex2(r.mo[nt][e] - mo_ref);
+      r.m[nt][e] = m_new;
+      r.mo[nt][e] = mo_new;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        r.acc[nt][d][e] *= f;
+        r.acc[nt][d][2 + e] *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float x = s[nt][i][2 * u + e];
+          r.l[nt][e] += ex2(x - m_ref);
+          s[nt][i][2 * u + e] = ex2(x + ve[i][u] - mo_ref);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      pb[nt][i][0] = transpose8x8(pack_half2(s[nt][i][0], s[nt][i][1]));
+      pb[nt][i][1] = transpose8x8(pack_half2(s[nt][i][2], s[nt][i][3]));
+    }
+  }
+  // ---- a NaN among the values of a key that only some rows keep must not reach the others (0 * NaN):
+  // those bytes are taken as 0, and the rows that keep them get their NaN from a product of indicators
+  uint32_t bad = 0;
+  if (MASK) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) bad |= nan_bytes(vf.x[i][u][w]);
+    bad = __any_sync(0xffffffffu, bad != 0);
+  }
+  // ---- O^T += V^T P^T
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      uint32_t v0 = vf.x[i][0][w], v1 = vf.x[i][1][w], v2 = vf.x[i][2][w], v3 = vf.x[i][3][w];
+      if (MASK && bad) {
+        v0 &= ~((nan_bytes(v0) >> 7) * 0xffu);
+        v1 &= ~((nan_bytes(v1) >> 7) * 0xffu);
+        v2 &= ~((nan_bytes(v2) >> 7) * 0xffu);
+        v3 &= ~((nan_bytes(v3) >> 7) * 0xffu);
+      }
+      const uint32_t lo01 = __byte_perm(v0, v1, 0x5140), hi01 = __byte_perm(v0, v1, 0x7362);
+      const uint32_t lo23 = __byte_perm(v2, v3, 0x5140), hi23 = __byte_perm(v2, v3, 0x7362);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma16816(r.acc[nt][2 * w], cvt_e4m3x2(lo01), cvt_e4m3x2_hi(lo01), cvt_e4m3x2(lo23),
+                 cvt_e4m3x2_hi(lo23), pb[nt][i][0], pb[nt][i][1]);
+        mma16816(r.acc[nt][2 * w + 1], cvt_e4m3x2(hi01), cvt_e4m3x2_hi(hi01), cvt_e4m3x2(hi23),
+                 cvt_e4m3x2_hi(hi23), pb[nt][i][0], pb[nt][i][1]);
+      }
+    }
+  if (MASK && bad) {
+    for (int nt = 0; nt < NT; ++nt) {
+      for (int w = 0; w < D / 32; ++w) {
+        float hit[2][4] = {};
+        for (int i = 0; i < 2; ++i) {
+          // e4m3 1.0 (0x38) where the byte is NaN; fp16 1.0 where the row keeps the key
+          uint32_t x[4];
+          for (int u = 0; u < 4; ++u) x[u] = (nan_bytes(vf.x[i][u][w]) >> 7) * 0x38u;
+          const uint32_t lo01 = __byte_perm(x[0], x[1], 0x5140), hi01 = __byte_perm(x[0], x[1], 0x7362);
+          const uint32_t lo23 = __byte_perm(x[2], x[3], 0x5140), hi23 = __byte_perm(x[2], x[3], 0x7362);
+          const uint32_t kb = keep >> (nt * 8 + i * 4);
+          const uint32_t b0 = transpose8x8((kb & 1 ? 0x3c00u : 0u) | (kb & 2 ? 0x3c000000u : 0u));
+          const uint32_t b1 = transpose8x8((kb & 4 ? 0x3c00u : 0u) | (kb & 8 ? 0x3c000000u : 0u));
+          mma16816(hit[0], cvt_e4m3x2(lo01), cvt_e4m3x2_hi(lo01), cvt_e4m3x2(lo23), cvt_e4m3x2_hi(lo23), b0, b1);
+          mma16816(hit[1], cvt_e4m3x2(hi01), cvt_e4m3x2_hi(hi01), cvt_e4m3x2(hi23), cvt_e4m3x2_hi(hi23), b0, b1);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int z = 0; z < D / 16; ++z)  // acc[nt][2 w + half], without a runtime register index
+            if ((z >> 1) == w && hit[z & 1][c] > 0.f) r.acc[nt][z][c] = __uint_as_float(0x7fffffffu);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ rows of a row tile
+template <int D, int NT>
+__device__ __forceinline__ void begin_rows(const PagedAttnParams& p, RowState<D, NT>& r, const SeqInfo& q, int h,
+                                           int rt, int g, int t) {
+  constexpr int R = 8 * NT;
+  const int rows = q.nq * p.G;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    // fragment row g
+    const int row = rt * R + nt * 8 + g;
+    float x[D / 4];
+    float top = 0.f;
+    if (row < rows) {
+      const int i = row / p.G, hq = h * p.G + row - i * p.G;
+      const long long off = (long long)(q.tok0 + i) * p.q_tok + (long long)hq * p.q_head;
+#pragma unroll
+      for (int z = 0; z < D / 64; ++z)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off + z * 64 + t * 16 + y * 8);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float2 f;
+            if (p.bf16) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ws[c]));
+            else f = __half22float2(*reinterpret_cast<const __half2*>(&ws[c]));
+            x[z * 16 + y * 8 + 2 * c] = f.x;
+            x[z * 16 + y * 8 + 2 * c + 1] = f.y;
+          }
+        }
+    } else {
+#pragma unroll
+      for (int z = 0; z < D / 4; ++z) x[z] = 0.f;
+    }
+#pragma unroll
+    for (int z = 0; z < D / 4; ++z) {
+      const float a = fabsf(x[z]);
+      if (a <= 3.402823466e38f) top = fmaxf(top, a);
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // largest magnitude to [2^13, 2^14): room for 28 further binades before fp16 ends
+    const int ex = (int)(__float_as_uint(top) >> 23) - 127;  // 0 -> -127
+    const int sh = max(-110, min(110, 13 - ex));
+    const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
+#pragma unroll
+    for (int z = 0; z < D / 16; ++z)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) r.q[nt][z][y] = pack_half2(x[z * 4 + y * 2] * up, x[z * 4 + y * 2 + 1] * up);
+    const float down = __uint_as_float((uint32_t)(127 - sh) << 23) * p.scale_log2;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int re = rt * R + nt * 8 + 2 * t + e;
+      r.qs[nt][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
+      r.live[nt][e] = re < rows;
+      r.pos[nt][e] = q.lead + re / p.G;
+      r.m[nt][e] = r.mo[nt][e] = -INFINITY;
+      r.l[nt][e] = 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) r.acc[nt][d][c] = 0.f;
+  }
+}
+
+__device__ __forceinline__ void store_out(const PagedAttnParams& p, long long at, float a, float b) {
+  uint32_t w;
+  if (p.bf16) w = pack_bf16x2(a, b);
+  else w = pack_half2(a, b);
+  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = w;
+}
+// acc * 2^(mo - m) / l: the exponent split in two, so that neither factor leaves fp32 where their
+// product does not
+__device__ __forceinline__ float2 join_factors(float mo, float m, float l) {
+  const float x = mo - m, h = rintf(0.5f * x);
+  return make_float2(ex2(h), ex2(x - h) / l);
+}
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Part of a row tile in the workspace: [R][D] accumulators, then [R][4] of mo, m, l.
+template <int D, int R>
+__device__ __forceinline__ float* part_of(const PagedAttnParams& p, int warp, int slot) {
+  return p.part + ((size_t)warp * 2 + slot) * (R * (D + 4));
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void end_rows(const PagedAttnParams& p, RowState<D, NT>& r, const SeqInfo& q, int h,
+                                         int rt, int g, int t, bool whole, float* part) {
+  constexpr int R = 8 * NT;
+  const int rows = q.nq * p.G;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = r.l[nt][e];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      const int lr = nt * 8 + 2 * t + e, row = rt * R + lr;
+      if (row >= rows) continue;
+      if (whole) {
+        const int i = row / p.G, hq = h * p.G + row - i * p.G;
+        const bool none = r.m[nt][e] == -INFINITY && !(l != l);
+        float2 f = join_factors(r.mo[nt][e], r.m[nt][e], l);
+        if (none || r.mo[nt][e] == -INFINITY) f = make_float2(0.f, none ? 0.f : 1.f / l);
+        const long long at = ((long long)(q.tok0 + i) * p.Hq + hq) * D + g * (D / 8);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+          store_out(p, at + 2 * d, none ? 0.f : r.acc[nt][d][e] * f.x * f.y, none ? 0.f : r.acc[nt][d][2 + e] * f.x * f.y);
+        if (g == 0 && p.lse)
+          p.lse[(long long)(q.tok0 + i) * p.Hq + hq] = none ? -INFINITY : (r.m[nt][e] + log2f(l)) * kLn2;
+      } else {
+        float* a = part + (size_t)lr * D + g * (D / 8);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+          *reinterpret_cast<float2*>(a + 2 * d) = make_float2(r.acc[nt][d][e], r.acc[nt][d][2 + e]);
+        if (g == 0)
+          *reinterpret_cast<float4*>(part + (size_t)R * D + lr * 4) = make_float4(r.mo[nt][e], r.m[nt][e], l, 0.f);
+      }
+    }
+}
+
+// ------------------------------------------------------------------ window tiles
+// Pages of a sequence, 32 at a time: lane x holds page first + x.
+struct PageRun {
+  int first;
+  uint32_t row;  // first row of the page for this head (id * Hkv + h) * P, kNoRow: none
+  float ks, ve;
+};
+__device__ __forceinline__ PageRun load_pages(const PagedAttnParams& p, int seq, int h, int first, int len, int lane) {
+  PageRun r;
+  r.first = first;
+  r.row = kNoRow;
+  r.ks = 0.f;
+  r.ve = 0.f;
+  const int pg = first + lane;
+  if (pg < p.max_pages && ((long long)pg << p.log_page) < len) {
+    const int id = __ldg(p.table + (long long)seq * p.max_pages + pg);
+    if (id >= 0 && id < p.num_pages) {
+      const size_t sc = (size_t)id * p.Hkv + h;
+      r.row = (uint32_t)(sc << p.log_page);
+      r.ks = __ldg(p.k_scale + sc);
+      r.ve = log2_of_scale(__ldg(p.v_scale + sc));
+    } else {
+      record_failure(p.err, nullptr, SEP_ERR_INDEX);
+    }
+  }
+  return r;
+}
+
+// Rows of 32 consecutive keys from c0 (a multiple of 32) for this lane's fragments.
+__device__ __forceinline__ void dense_rows(const PagedAttnParams& p, const PageRun& pr, int c0, int end, int g, int t,
+                                           uint32_t (&kr)[2][2], uint32_t (&vr)[2][4],
+                                           float (&ks)[2][2], float (&ve)[2][2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int x = c0 + 16 * i;
+    const int src = ((x >> p.log_page) - pr.first) & 31;
+    const uint32_t base = __shfl_sync(0xffffffffu, pr.row, src);
+    const float s = __shfl_sync(0xffffffffu, pr.ks, src), e = __shfl_sync(0xffffffffu, pr.ve, src);
+    const uint32_t row = base + (uint32_t)(x & ((1 << p.log_page) - 1));
+    const int left = base == kNoRow ? 0 : min(16, end - x);  // rows of this tile that exist
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      kr[i][u] = 8 * u + g < left ? row + 8 * u + g : kNoRow;
+      ks[i][u] = s;
+      ve[i][u] = e;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int y = 2 * t + (u & 1) + 8 * (u >> 1);
+      vr[i][u] = y < left ? row + y : kNoRow;
+    }
+  }
+}
+
+// Keys [c0, c1) of the window part (c0 a multiple of 64).
+template <int D, int NT>
+__device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int len,
+                                            int lo, int hi, int c0, int c1, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const int run = 32 << p.log_page;
+  PageRun pr = load_pages(p, seq, h, c0 >> p.log_page, len, lane);
+  KFrag<D> kf;
+  VFrag<D> vf;
+  uint32_t kr[2][2], vr[2][4];
+  float ks[2][2], ve[2][2], ksn[2][2], ven[2][2];
+  dense_rows(p, pr, c0, c1, g, t, kr, vr, ks, ve);
+  load_k(kf, p.k_pages, kr, t);
+  load_v(vf, p.v_pages, vr, g);
+  for (int c = c0; c < c1; c += 32) {
+    const bool more = c + 32 < c1;
+    int kpos[2][2];
+    bool anchor[2][2];
+    // every row keeps all 32 keys: none behind the earliest query, none outside the last one's window
+    const bool full = c + 32 <= c1 && c + 31 <= lo && hi - c < p.n &&
+                      __all_sync(0xffffffffu, kr[0][0] != kNoRow && kr[1][0] != kNoRow);
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = c + 16 * i + 8 * u + g;
+          kpos[i][u] = kr[i][u] != kNoRow ? j : -1;
+          anchor[i][u] = false;
+          if (kr[i][u] != kNoRow && hi - c >= p.n) {
+            const int id = (int)((kr[i][u] >> p.log_page) / (uint32_t)p.Hkv);
+            anchor[i][u] = j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + (j & ((1 << p.log_page) - 1))) != 0;
+          }
+        }
+      step32<D, NT, true>(p, r, kf, vf, ks, ve, kpos, anchor);
+    } else {
+      step32<D, NT, false>(p, r, kf, vf, ks, ve, kpos, anchor);
+    }
+    if (more) {
+      if (c + 32 - (pr.first << p.log_page) >= run) pr = load_pages(p, seq, h, (c + 32) >> p.log_page, len, lane);
+      dense_rows(p, pr, c + 32, c1, g, t, kr, vr, ksn, ven);
+      load_k(kf, p.k_pages, kr, t);
+      load_v(vf, p.v_pages, vr, g);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          ks[i][u] = ksn[i][u];
+          ve[i][u] = ven[i][u];
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ tiles left of the window
+// Positions [c0, c1) (at most kScan, c0 a multiple of kScan): the keys with j < a or a separator flag,
+// kept by every row, are listed in shared memory and read 32 at a time.
+struct Listed {
+  uint32_t row;
+  float ks, ve;
+};
+template <int D, int NT>
+__device__ __forceinline__ void scan_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int c0, int c1,
+                                          Listed* list, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  // 16 positions per lane: always inside one page
+  const int j0 = c0 + 16 * lane;
+  uint32_t bits = 0, row = 0;
+  float ks = 0.f, ve = 0.f;
+  if (j0 < c1) {
+    const int pg = j0 >> p.log_page;
+    const int id = pg < p.max_pages ? __ldg(p.table + (long long)seq * p.max_pages + pg) : -1;
+    if (id >= 0 && id < p.num_pages) {
+      const int off = (int)(j0 & ((1 << p.log_page) - 1));
+      const uint4 f = __ldg(reinterpret_cast<const uint4*>(p.flags + ((size_t)id << p.log_page) + off));
+      const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int x = 0; x < 16; ++x) bits |= ((w[x >> 2] >> (8 * (x & 3))) & 0xffu ? 1u : 0u) << x;
+      const int init = p.a - j0;  // initial tokens
+      if (init > 0) bits |= init >= 16 ? 0xffffu : (1u << init) - 1u;
+      const int left = c1 - j0;
+      if (left < 16) bits &= (1u << left) - 1u;
+      const size_t sc = (size_t)id * p.Hkv + h;
+      row = (uint32_t)(sc << p.log_page) + off;
+      ks = __ldg(p.k_scale + sc);
+      ve = log2_of_scale(__ldg(p.v_scale + sc));
+    } else {
+      record_failure(p.err, nullptr, SEP_ERR_INDEX);
+    }
+  }
+  const int cnt = __popc(bits);
+  int at = cnt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, at, 31);
+  at -= cnt;
+  __syncwarp();  // the list's last readers are done
+  while (bits) {
+    const int x = __ffs(bits) - 1;
+    bits &= bits - 1;
+    list[at++] = Listed{row + x, ks, ve};
+  }
+  __syncwarp();
+  KFrag<D> kf;
+  VFrag<D> vf;
+  uint32_t kr[2][2], vr[2][4];
+  for (int b = 0; b < total; b += 32) {
+    float kss[2][2], vee[2][2];
+    int kpos[2][2];
+    bool anchor[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int x = b + 16 * i + 8 * u + g;
+        const Listed e = list[min(x, total - 1)];
+        kr[i][u] = x < total ? e.row : kNoRow;
+        kss[i][u] = e.ks;
+        vee[i][u] = e.ve;
+        kpos[i][u] = x < total ? 0 : -1;  // position 0: behind no row with a position
+        anchor[i][u] = true;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = b + 16 * i + 2 * t + (u & 1) + 8 * (u >> 1);
+        vr[i][u] = x < total ? list[x].row : kNoRow;
+      }
+    }
+    load_k(kf, p.k_pages, kr, t);
+    load_v(vf, p.v_pages, vr, g);
+    if (b + 32 <= total) step32<D, NT, false>(p, r, kf, vf, kss, vee, kpos, anchor);
+    else step32<D, NT, true>(p, r, kf, vf, kss, vee, kpos, anchor);
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int R = 8 * NT;
+  extern __shared__ long long s_base[];  // [S + 1], then the scan lists of the warps
+  __shared__ long long s_part[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Listed* list = reinterpret_cast<Listed*>(s_base + p.S + 1) + warp * kScan;
+  grid_dep_wait();
+  grid_dep_launch_next();
+
+  // ---- first tile of every sequence (every CTA for itself; CTA 0 leaves them for the join)
+  long long carry = 0;
+  for (int s0 = 0; s0 < p.S; s0 += kWarps * 32) {
+    const int s = s0 + tid;
+    long long x = 0;
+    if (s < p.S) {
+      const SeqInfo q = seq_info(p, s);
+      x = (long long)tiles_per_row_tile(p, q, R) * row_tiles(p, q, R) * p.Hkv;
+      if (q.bad && blockIdx.x == 0) record_failure(p.err, nullptr, SEP_ERR_INDEX);
+    }
+    long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_part[warp] = inc;
+    __syncthreads();
+    long long before = carry;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_part[w];
+      carry += s_part[w];
+    }
+    if (s < p.S) s_base[s] = before + inc - x;
+    __syncthreads();
+  }
+  if (tid == 0) s_base[p.S] = carry;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int s = tid; s <= p.S; s += kWarps * 32) p.base[s] = s_base[s];
+  const long long total = carry;
+  const int gw = blockIdx.x * kWarps + warp;
+  // padding queries (sequences without a key) have no tile: their rows are written here
+  for (int s = gw; s < p.S; s += p.nwarps) {
+    const SeqInfo q = seq_info(p, s);
+    if (q.nq > 0 && q.len == 0) {
+      const long long at = (long long)q.tok0 * p.Hq, cnt = (long long)q.nq * p.Hq;
+      for (long long e = lane; e < cnt * (D / 2); e += 32)
+        reinterpret_cast<uint32_t*>(p.o)[at * (D / 2) + e] = 0u;
+      if (p.lse)
+        for (long long e = lane; e < cnt; e += 32) p.lse[at + e] = -INFINITY;
+    }
+  }
+  const long long per = (total + p.nwarps - 1) / p.nwarps;
+  long long x = (long long)gw * per;
+  const long long x_end = min(total, x + per);
+  if (x >= x_end) return;
+
+  // ---- sequence of tile x: last s with s_base[s] <= x (sequences without tiles share a start)
+  int s_lo = 0, s_hi = p.S;
+  while (s_hi - s_lo > 1) {
+    const int mid = (s_lo + s_hi) >> 1;
+    if (s_base[mid] <= x) s_lo = mid;
+    else s_hi = mid;
+  }
+  int seq = s_lo;
+  RowState<D, NT> r;
+  const int g = lane >> 2, t = lane & 3;
+  bool first_segment = true;
+  while (x < x_end) {
+    while (s_base[seq + 1] <= x) ++seq;
+    const SeqInfo q = seq_info(p, seq);
+    const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+    const long long unit = (x - s_base[seq]) / per_rt;
+    const int ta = (int)((x - s_base[seq]) - unit * per_rt);
+    const int tb = (int)min((long long)per_rt, ta + (x_end - x));
+    const int h = (int)(unit / nrt), rt = (int)(unit - (long long)h * nrt);
+    const RowTile w = row_tile(p, q, rt, R);
+    begin_rows<D, NT>(p, r, q, h, rt, g, t);
+    for (int y = ta; y < min(tb, w.ns); ++y)
+      scan_keys<D, NT>(p, r, seq, h, y * kScan, min(w.w0, (y + 1) * kScan), list, lane);
+    const int da = max(ta, w.ns) - w.ns, db = min(tb - w.ns, w.nd);
+    if (da < db) {
+      const int lo = q.lead + rt * R / p.G;
+      const int hi = q.lead + min(q.nq - 1, (rt * R + R - 1) / p.G);
+      window_keys<D, NT>(p, r, seq, h, q.len, lo, hi, w.w0 + da * kDense,
+                         min(w.kend, w.w0 + db * kDense), lane);
+    }
+    const bool whole = ta == 0 && tb == per_rt;
+    // a warp's run has at most one row tile that began before it (slot 0) and one that ends after it
+    end_rows<D, NT>(p, r, q, h, rt, g, t, whole, whole ? nullptr : part_of<D, R>(p, gw, first_segment ? 0 : 1));
+    first_segment = false;
+    x += tb - ta;
+  }
+}
+
+// ------------------------------------------------------------------ join of the parts
+// One CTA per (query token, query head). Its row tile's tiles belong to warps w0 .. w1; with w0 = w1
+// the row is written already. Part of warp w0 is in its slot 1 unless its run begins with this row
+// tile; the others begin with it (slot 0).
+template <int D, int NT>
+__global__ void __launch_bounds__(128) seppaged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int R = 8 * NT, LPR = D / 4, GR = 128 / LPR;  // lanes per row, groups of lanes
+  __shared__ float4 s_acc[GR][LPR];
+  __shared__ float s_st[GR][3];
+  grid_dep_wait();
+  grid_dep_launch_next();
+  const int tok = blockIdx.x / p.Hq, hq = blockIdx.x - tok * p.Hq;
+  const int tid = threadIdx.x;
+  // sequence of the token: last s with indptr[s] <= tok
+  int lo = 0, hi = p.S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.indptr + mid) <= tok) lo = mid;
+    else hi = mid;
+  }
+  const SeqInfo q = seq_info(p, lo);
+  if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
+  const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
+  const int rt = row / R, lr = row - rt * R;
+  const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+  const long long t0 = p.base[lo] + ((long long)h * nrt + rt) * per_rt, t1 = t0 + per_rt;
+  const long long per = (p.base[p.S] + p.nwarps - 1) / p.nwarps;
+  const int w0 = (int)(t0 / per), w1 = (int)((t1 - 1) / per);
+  if (w0 == w1) return;
+  const int grp = tid / LPR, c = tid - grp * LPR;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float mo = -INFINITY, m = -INFINITY, l = 0.f;
+  auto add = [&](float4 a, float mo2, float m2, float l2) {
+    const float mo_n = fmaxf(mo, mo2), m_n = fmaxf(m, m2);
+    const float mor = mo_n == -INFINITY ? 0.f : mo_n, mr = m_n == -INFINITY ? 0.f : m_n;
+    const float f0 = ex2(mo - mor), f1 = ex2(mo2 - mor);
+    l = l * ex2(m - mr) + l2 * ex2(m2 - mr);
+    acc.x = acc.x * f0 + a.x * f1;
+    acc.y = acc.y * f0 + a.y * f1;
+    acc.z = acc.z * f0 + a.z * f1;
+    acc.w = acc.w * f0 + a.w * f1;
+    mo = mo_n;
+    m = m_n;
+  };
+#pragma unroll 4
+  for (int w = w0 + grp; w <= w1; w += GR) {
+    const float* part = part_of<D, R>(p, w, w == w0 && t0 > (long long)w0 * per ? 1 : 0);
+    const float4 st = *reinterpret_cast<const float4*>(part + (size_t)R * D + lr * 4);
+    const float4 a = *reinterpret_cast<const float4*>(part + (size_t)lr * D + c * 4);
+    add(a, st.x, st.y, st.z);
+  }
+  s_acc[grp][c] = acc;
+  if (c == 0) {
+    s_st[grp][0] = mo;
+    s_st[grp][1] = m;
+    s_st[grp][2] = l;
+  }
+  __syncthreads();
+  if (grp != 0) return;
+  for (int x = 1; x < GR; ++x) add(s_acc[x][c], s_st[x][0], s_st[x][1], s_st[x][2]);
+  const bool none = m == -INFINITY && !(l != l);
+  float2 f = join_factors(mo, m, l);
+  if (none || mo == -INFINITY) f = make_float2(0.f, none ? 0.f : 1.f / l);
+  const long long at = ((long long)tok * p.Hq + hq) * D + c * 4;
+  store_out(p, at, none ? 0.f : acc.x * f.x * f.y, none ? 0.f : acc.y * f.x * f.y);
+  store_out(p, at + 2, none ? 0.f : acc.z * f.x * f.y, none ? 0.f : acc.w * f.x * f.y);
+  if (c == 0 && p.lse) p.lse[(long long)tok * p.Hq + hq] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D, int NT>
+cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
+  const size_t smem = (size_t)(p.S + 1) * sizeof(long long) + (size_t)kWarps * kScan * sizeof(Listed);
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !set[dev].load()) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev].store(true);
+  }
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_attn_kernel<D, NT>, kWarps * 32, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(kMaxWarps / kWarps, 148 * std::max(per_sm, 1));
+  p.nwarps = grid * kWarps;
+  e = launch_chained(paged_attn_kernel<D, NT>, dim3(grid), dim3(kWarps * 32), smem, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_chained(seppaged_join_kernel<D, NT>, dim3((unsigned)p.T * p.Hq), dim3(128), 0, stream, p);
+}
+
+}  // namespace
+
+// Workspace: [S + 1] tile numbers, then two parts per warp (32-row tiles at most).
+size_t paged_attn_workspace(int S, int d) {
+  const size_t base = ((size_t)(S + 1) * sizeof(long long) + 255) / 256 * 256;
+  return base + (size_t)kMaxWarps * 2 * 16 * (d + 4) * sizeof(float);
+}
+
+cudaError_t launch_paged_attn(const SepPagedState& st, int dtype, const void* q, long long q_tok, long long q_head,
+                              int Hq, int T, int S, int max_pages, const int32_t* table, const int32_t* lens,
+                              const int32_t* indptr, int a, int n, float scale, void* o, float* lse, void* ws,
+                              cudaStream_t stream) {
+  PagedAttnParams p = {};
+  p.k_pages = st.k_pages;
+  p.v_pages = st.v_pages;
+  p.k_scale = st.k_scale;
+  p.v_scale = st.v_scale;
+  p.flags = st.flags;
+  p.q = q;
+  p.q_tok = q_tok;
+  p.q_head = q_head;
+  p.o = o;
+  p.lse = lse;
+  p.table = table;
+  p.lens = lens;
+  p.indptr = indptr;
+  p.base = static_cast<long long*>(ws);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)(S + 1) * sizeof(long long) + 255) / 256 * 256);
+  p.err = device_error_word();
+  p.T = T;
+  p.S = S;
+  p.Hq = Hq;
+  p.Hkv = st.Hkv;
+  p.G = Hq / st.Hkv;
+  p.num_pages = st.num_pages;
+  p.max_pages = max_pages;
+  p.log_page = 31 - __builtin_clz((unsigned)st.page);
+  p.a = a;
+  p.n = n;
+  p.bf16 = dtype == SEP_DTYPE_BF16;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  // 16-row tiles once the sequences have more than 8 (token, head) rows on average: keys are then
+  // converted once for 16 rows instead of 8
+  const bool wide = (long long)T * p.G > 8ll * S;
+  if (st.d == 128)
+    return wide ? launch_paged_attn_t<128, 2>(p, stream) : launch_paged_attn_t<128, 1>(p, stream);
+  return wide ? launch_paged_attn_t<64, 2>(p, stream) : launch_paged_attn_t<64, 1>(p, stream);
+}
+
+}  // namespace sep

@@ -90,4 +90,21 @@ cudaError_t launch_sepcache_decode(const SepCacheState& st, const void* q, void*
 cudaError_t launch_sepcache_export(const SepCacheState& st, int32_t* pos_out, int32_t* count,
                                    cudaStream_t stream);
 
+// Rotation of q and (unless null) k; sign -1 turns the other way (gradients).
+cudaError_t launch_rope(const SepRope& r, int dtype, int B, int L, int d, const void* pos, int pos64,
+                        long long pos_stride, const SepRopeTensor* q, const SepRopeTensor* k,
+                        float sign, cudaStream_t stream);
+
+cudaError_t launch_paged_append(const SepPagedState& st, int dtype, const void* k, long long k_tok,
+                                long long k_head, const void* v, long long v_tok, long long v_head,
+                                const uint8_t* sep, int T, int S, int max_pages,
+                                const int32_t* table, const int32_t* lens, const int32_t* indptr,
+                                cudaStream_t stream);
+size_t paged_attn_workspace(int S, int d);
+cudaError_t launch_paged_attn(const SepPagedState& st, int dtype, const void* q, long long q_tok,
+                              long long q_head, int Hq, int T, int S, int max_pages,
+                              const int32_t* table, const int32_t* lens, const int32_t* indptr,
+                              int a, int n, float scale, void* o, float* lse, void* ws,
+                              cudaStream_t stream);
+
 }  // namespace sep

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -31,6 +32,7 @@ def _load():
             f"{_LIB_PATH} is missing: build it with `python -m kv_cache_compression_sep_b200.build`")
     lib = ctypes.CDLL(_LIB_PATH)
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    L = ctypes.c_int64
     sig = {
         "sep_mask_build": (I, [P, I, I, I, I, I, I, P, P, P, P, P, P, P]),
         "sep_attn_fwd_workspace_size": (Z, [I, I, I, I]),
@@ -45,6 +47,11 @@ def _load():
         "sepcache_decode": (I, [P, P, P, P, F, P]),
         "sepcache_prefill": (I, [P, P, P, P, I, P]),
         "sepcache_export_order": (I, [P, P, P, P]),
+        "sep_rope_fwd": (I, [P, I, I, I, I, P, I, L, P, P, P]),
+        "sep_rope_bwd": (I, [P, I, I, I, I, P, I, L, P, P, P]),
+        "seppaged_append": (I, [P, I, P, L, L, P, L, L, P, I, I, I, P, P, P, P]),
+        "seppaged_attn_workspace_size": (Z, [I, I]),
+        "seppaged_attn": (I, [P, I, P, L, L, I, I, I, I, P, P, P, I, I, F, P, P, P, Z, P]),
         "sep_last_device_error": (I, []),
         "sep_set_wait_limit_ns": (I, [ctypes.c_ulonglong]),
         "sep_status_string": (ctypes.c_char_p, [I]),
@@ -75,6 +82,23 @@ class _SepCacheState(ctypes.Structure):
                 ("k_slots", ctypes.c_void_p), ("v_slots", ctypes.c_void_p),
                 ("slot_pos", ctypes.c_void_p), ("slot_sep", ctypes.c_void_p),
                 ("meta", ctypes.c_void_p), ("rope_freq", ctypes.c_void_p)]
+
+
+class _SepRope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("d_rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class _SepRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
+                ("y_stride", ctypes.c_int64 * 3), ("H", ctypes.c_int32)]
+
+
+class _SepPagedState(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("flags", ctypes.c_void_p), ("rope", _SepRope)]
 
 
 def _check(status: int, what: str):
@@ -402,3 +426,374 @@ class SepCache:
         _check(_lib.sepcache_export_order(ctypes.byref(self._st), _ptr(pos), _ptr(cnt),
                                           _stream()), "sepcache_export_order")
         return pos, cnt
+
+
+# ------------------------------------------------------------------ rotary positions
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+INT32_MAX = 2 ** 31 - 1
+
+
+def _strided(t, dtypes, name, shape):
+    """t must be a CUDA tensor of this shape and one of these dtypes, its last dimension
+    contiguous; the other strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise SepError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise SepError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise SepError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise SepError(f"{name}: the last dimension must be contiguous")
+    if not t.is_cuda:
+        raise SepError(f"{name} must be on a CUDA device (there is no CPU path)")
+
+
+@dataclasses.dataclass
+class SepRope:
+    """Rotation parameters: angles per position step (fp64, on the device), layout, magnitude."""
+    freq: torch.Tensor
+    d_rot: int
+    interleaved: bool
+    magnitude: float
+
+    def _c(self):
+        return _SepRope(self.freq.data_ptr(), self.d_rot, int(self.interleaved), self.magnitude)
+
+
+def _scaled_frequencies(d_rot, theta, scaling):
+    """(list of d_rot / 2 inverse frequencies, magnitude factor), in fp64 on the host.
+
+    With w = theta^(-2z / d_rot) and factor s:
+      linear  w / s (positions interpolated);
+      ntk     the base becomes theta s^(d_rot / (d_rot - 2));
+      llama3  wavelengths 2 pi / w above original_max_position / low_freq_factor are divided by s,
+              those below original_max_position / high_freq_factor kept, linear in between;
+      yarn    between the pairs that turn beta_fast and beta_slow times over
+              original_max_position positions a linear ramp from w to w / s; the magnitude is
+              attention_factor, by default 0.1 ln s + 1.
+    """
+    w = [theta ** (-2.0 * z / d_rot) for z in range(d_rot // 2)]
+    if scaling is None:
+        return w, 1.0
+    opt = dict(scaling)
+    kind = opt.pop("type", None)
+    allowed = {"linear": {"factor"}, "ntk": {"factor"},
+               "llama3": {"factor", "low_freq_factor", "high_freq_factor",
+                          "original_max_position"},
+               "yarn": {"factor", "original_max_position", "beta_fast", "beta_slow",
+                        "attention_factor"}}
+    if kind not in allowed:
+        raise SepError(f"scaling type {kind!r}: one of {sorted(allowed)}")
+    if set(opt) - allowed[kind]:
+        raise SepError(f"scaling {kind}: unknown {sorted(set(opt) - allowed[kind])}")
+    try:
+        s = float(opt["factor"])
+        if kind in ("llama3", "yarn"):
+            length = float(opt["original_max_position"])
+        if kind == "llama3":
+            low, high = float(opt["low_freq_factor"]), float(opt["high_freq_factor"])
+    except KeyError as e:
+        raise SepError(f"scaling {kind} needs {e}") from None
+    if not s >= 1.0:
+        raise SepError(f"scaling factor {s} must be at least 1")
+    if kind == "linear":
+        return [x / s for x in w], 1.0
+    if kind == "ntk":
+        if d_rot < 4:
+            raise SepError("ntk scaling needs d_rot of at least 4")
+        base = theta * s ** (d_rot / (d_rot - 2.0))
+        return [base ** (-2.0 * z / d_rot) for z in range(d_rot // 2)], 1.0
+    if not length > 0.0:
+        raise SepError("original_max_position must be positive")
+    if kind == "llama3":
+        if not 0.0 < low < high:
+            raise SepError("llama3 scaling needs 0 < low_freq_factor < high_freq_factor")
+        out = []
+        for x in w:
+            keep = min(max((length * x / (2.0 * math.pi) - low) / (high - low), 0.0), 1.0)
+            out.append((1.0 - keep) * x / s + keep * x)
+        return out, 1.0
+    fast, slow = float(opt.get("beta_fast", 32.0)), float(opt.get("beta_slow", 1.0))
+    if not fast > slow > 0.0 or not theta > 1.0:
+        raise SepError("yarn scaling needs beta_fast > beta_slow > 0 and theta > 1")
+
+    def pair_of(turns):
+        return d_rot * math.log(length / (turns * 2.0 * math.pi)) / (2.0 * math.log(theta))
+
+    lo = max(math.floor(pair_of(fast)), 0)
+    hi = min(math.ceil(pair_of(slow)), d_rot - 1)
+    out = []
+    for z, x in enumerate(w):
+        ramp = min(max((z - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+        out.append(x / s * ramp + x * (1.0 - ramp))
+    magnitude = opt.get("attention_factor")
+    return out, float(0.1 * math.log(s) + 1.0 if magnitude is None else magnitude)
+
+
+def sep_rope_table(d_rot, theta, interleaved=False, scaling=None, device="cuda") -> SepRope:
+    """Rotation of the first d_rot elements of a head with base theta; kept across calls.
+
+    scaling: None or a dict with "type" linear, ntk, llama3 or yarn and its parameters
+    (factor, original_max_position, low_freq_factor, high_freq_factor, beta_fast, beta_slow,
+    attention_factor)."""
+    if int(d_rot) != d_rot or d_rot < 2 or d_rot % 2 != 0:
+        raise SepError(f"d_rot = {d_rot} must be an even number of at least 2")
+    if not theta > 0.0:
+        raise SepError(f"theta = {theta} must be positive")
+    freq, magnitude = _scaled_frequencies(int(d_rot), float(theta), scaling)
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise SepError(f"the table must live on a CUDA device, not {dev} (there is no CPU path)")
+    return SepRope(torch.tensor(freq, dtype=torch.float64, device=dev), int(d_rot),
+                   bool(interleaved), magnitude)
+
+
+def _rope_call(fn, what, q, k, positions, rope, out):
+    if not isinstance(rope, SepRope):
+        raise SepError("rope must come from sep_rope_table")
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise SepError("q must be a [tokens, heads, d] or [B, L, heads, d] tensor")
+    lead, d = tuple(q.shape[:-2]), q.shape[-1]
+    if rope.d_rot > d:
+        raise SepError(f"d_rot = {rope.d_rot} is larger than the head dimension {d}")
+    tensors = [("q", q)] if k is None else [("q", q), ("k", k)]
+    for name, t in tensors:
+        heads = t.shape[-2] if isinstance(t, torch.Tensor) and t.dim() == q.dim() else 0
+        _strided(t, tuple(_DTYPES), name, lead + (heads, d))
+        if t.dtype != q.dtype:
+            raise SepError(f"{name} has dtype {t.dtype}, q has {q.dtype}")
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+        raise SepError("positions must be an int32 or int64 tensor")
+    if tuple(positions.shape) not in (lead, lead[-1:]):
+        raise SepError(f"positions has shape {tuple(positions.shape)}, expected {lead} "
+                       f"or {lead[-1:]}")
+    if not positions.is_contiguous():
+        raise SepError("positions must be contiguous")
+    if not positions.is_cuda:
+        raise SepError("positions must be on a CUDA device (there is no CPU path)")
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for _, t in tensors)
+    out = tuple(x for x in (out if isinstance(out, (tuple, list)) else (out,)) if x is not None)
+    if len(out) != len(tensors):
+        raise SepError(f"out must hold {len(tensors)} tensor(s)")
+    for (name, t), y in zip(tensors, out):
+        _strided(y, (q.dtype,), f"out {name}", t.shape)
+        if any(n > 1 and x == 0 for n, x in zip(y.shape, y.stride())):
+            raise SepError(f"out {name} is an expanded view: its rows share memory")
+        if y.data_ptr() != t.data_ptr() and _overlap(t, y):
+            raise SepError(f"out {name} overlaps {name} without being it")
+        if y.data_ptr() == t.data_ptr() and y.stride() != t.stride() and t.numel() > 0:
+            raise SepError(f"out {name} starts where {name} does with other strides")
+    _same_device(q.device, *tensors, *((f"out {n}", y) for (n, _), y in zip(tensors, out)),
+                 ("positions", positions), ("rope", rope.freq))
+    result = out if k is not None else (out[0], None)
+    if q.numel() == 0 and (k is None or k.numel() == 0):
+        return result
+    if any(t.numel() == 0 for _, t in tensors):
+        raise SepError("q and k need at least one head each")
+    B, L = (1, lead[0]) if len(lead) == 1 else lead
+    if B * L > INT32_MAX:
+        raise SepError("more than 2^31 - 1 tokens")
+    args = []
+    for (_, t), y in zip(tensors, out):
+        xs, ys = ((0,) + s if len(lead) == 1 else s for s in (t.stride()[:-1], y.stride()[:-1]))
+        args.append(_SepRopeTensor(t.data_ptr(), y.data_ptr(), (ctypes.c_int64 * 3)(*xs),
+                                   (ctypes.c_int64 * 3)(*ys), t.shape[-2]))
+    rc = rope._c()
+    _check(fn(ctypes.byref(rc), _DTYPES[q.dtype], B, L, d, _ptr(positions),
+              int(positions.dtype == torch.int64), L if positions.dim() == 2 else 0,
+              ctypes.byref(args[0]), ctypes.byref(args[1]) if len(args) > 1 else None, _stream()),
+           what)
+    return result
+
+
+def _extent(t):
+    """First and last byte address (exclusive) of a tensor with non-negative strides."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _overlap(x, y):
+    """Whether the address ranges of two tensors meet. Views that interleave inside one buffer
+    (q and v of a fused projection) count as overlapping unless their rows cannot meet: same
+    strides and starts that differ by less than the smallest stride hold disjoint rows."""
+    if x.numel() == 0 or y.numel() == 0:
+        return False
+    (a0, a1), (b0, b1) = _extent(x), _extent(y)
+    if a1 <= b0 or b1 <= a0:
+        return False
+    if x.stride() == y.stride() and x.shape[:-2] == y.shape[:-2]:
+        # one token's heads form a block; blocks of x and y alternate with the token stride
+        size = x.element_size()
+        block = ((x.shape[-2] - 1) * x.stride(-2) + x.shape[-1]) * size
+        outer = [s * size for n, s in zip(x.shape[:-2], x.stride()[:-2]) if n > 1]
+        if outer:
+            step = min(outer)
+            gap = (b0 - a0) % step
+            if all(s % step == 0 for s in outer) and block <= gap and gap + block <= step:
+                return False
+    return True
+
+
+def sep_rope_fwd(q, k, positions, rope: SepRope, out=None):
+    """Rotary positions on q [B, L, Hq, d] and k [B, L, Hkv, d] (or [T, H, d] each; k may be None).
+
+    bf16, fp16 or fp32; heads contiguous, other strides free. positions [B, L] (or [L], shared by
+    the batch; [T]) int32 or int64. out: (q', k') to write to, which may be q and k themselves.
+    Returns (q', k')."""
+    return _rope_call(_lib.sep_rope_fwd, "sep_rope_fwd", q, k, positions, rope, out)
+
+
+def sep_rope_bwd(dq, dk, positions, rope: SepRope, out=None):
+    """Gradients of sep_rope_fwd's inputs from those of its outputs (same arguments)."""
+    return _rope_call(_lib.sep_rope_bwd, "sep_rope_bwd", dq, dk, positions, rope, out)
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+class SepPagedCache:
+    """Paged cache of e4m3 keys and values with one power-of-two scale per (page, KV head).
+
+    num_pages pages of `page` tokens (16, 32, 64 or 128); rope: rotation applied to appended keys
+    at their positions (None: keys are stored as given). The page table, lengths and token offsets
+    belong to the caller and are passed to each call as device tensors:
+      page_table [S, max_pages] int32, seq_lens [S] int32 (the call's new tokens included),
+      indptr [S + 1] int32 (tokens indptr[s] .. indptr[s + 1] - 1 of the call are sequence s's
+      newest).
+    Methods map one-to-one to seppaged_append / seppaged_attn.
+    """
+
+    def __init__(self, num_pages, Hkv, d, page=64, rope: SepRope | None = None, device="cuda"):
+        if num_pages < 1 or Hkv < 1:
+            raise SepError("num_pages and Hkv must be positive")
+        if d not in (64, 128):
+            raise SepError(f"head dimension {d}: 64 or 128")
+        if page not in (16, 32, 64, 128):
+            raise SepError(f"page size {page}: 16, 32, 64 or 128")
+        if num_pages * Hkv * page >= 2 ** 32:
+            raise SepError("num_pages * Hkv * page must be below 2^32")
+        if rope is not None and not isinstance(rope, SepRope):
+            raise SepError("rope must come from sep_rope_table")
+        if rope is not None and rope.d_rot > d:
+            raise SepError(f"d_rot = {rope.d_rot} is larger than the head dimension {d}")
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise SepError(f"SepPagedCache must live on a CUDA device, not {dev} "
+                           "(there is no CPU path)")
+        self.num_pages, self.Hkv, self.d, self.page, self.rope = num_pages, Hkv, d, page, rope
+        shape = (num_pages, Hkv, page, d)
+        self.k_pages = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        self.v_pages = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        self.k_scale = torch.zeros(num_pages, Hkv, dtype=torch.float32, device=dev)
+        self.v_scale = torch.zeros(num_pages, Hkv, dtype=torch.float32, device=dev)
+        self.flags = torch.zeros(num_pages, page, dtype=torch.uint8, device=dev)
+
+    _STATE = ("k_pages", "v_pages", "k_scale", "v_scale", "flags")
+
+    def state_dict(self):
+        """Host copies of every state tensor (stream-ordered after earlier calls)."""
+        return {k: getattr(self, k).to("cpu", copy=True) for k in self._STATE}
+
+    def load_state_dict(self, sd):
+        """Restores a state_dict() taken from a cache of the same shape."""
+        for k in self._STATE:
+            dst = getattr(self, k)
+            if tuple(sd[k].shape) != tuple(dst.shape) or sd[k].dtype != dst.dtype:
+                raise SepError(f"load_state_dict: {k} has shape {tuple(sd[k].shape)}, "
+                               f"expected {tuple(dst.shape)}")
+            dst.copy_(sd[k])
+
+    def _c(self):
+        rope = _SepRope(None, 0, 0, 1.0) if self.rope is None else self.rope._c()
+        return _SepPagedState(self.num_pages, self.Hkv, self.d, self.page,
+                              self.k_pages.data_ptr(), self.v_pages.data_ptr(),
+                              self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                              self.flags.data_ptr(), rope)
+
+    def _plan(self, page_table, seq_lens, indptr):
+        """Checks the index tensors and the state; returns (S, max_pages)."""
+        S, max_pages = _dims(page_table, 2, "page_table")
+        _cuda(page_table, torch.int32, "page_table")
+        _cuda(seq_lens, torch.int32, "seq_lens", (S,))
+        _cuda(indptr, torch.int32, "indptr", (S + 1,))
+        if S < 1 or max_pages < 1:
+            raise SepError("page_table needs at least one sequence and one page")
+        _cuda(self.k_pages, torch.float8_e4m3fn, "k_pages",
+              (self.num_pages, self.Hkv, self.page, self.d))
+        _cuda(self.v_pages, torch.float8_e4m3fn, "v_pages", tuple(self.k_pages.shape))
+        _cuda(self.k_scale, torch.float32, "k_scale", (self.num_pages, self.Hkv))
+        _cuda(self.v_scale, torch.float32, "v_scale", (self.num_pages, self.Hkv))
+        _cuda(self.flags, torch.uint8, "flags", (self.num_pages, self.page))
+        return S, max_pages
+
+    def _on_device(self, *named):
+        _same_device(self.k_pages.device, *((k, getattr(self, k)) for k in self._STATE),
+                     ("rope", self.rope.freq if self.rope is not None else None), *named)
+
+    @staticmethod
+    def _rows(t, name):
+        """Token and head strides of a [T, H, d] tensor read 16 bytes at a time."""
+        if t.data_ptr() % 16 != 0 or t.stride(0) % 8 != 0 or t.stride(1) % 8 != 0:
+            raise SepError(f"{name}: the start and the strides of tokens and heads must be "
+                           "multiples of 16 bytes")
+        return t.stride(0), t.stride(1)
+
+    def seppaged_append(self, k, v, page_table, seq_lens, indptr, sep=None):
+        """Stores the newest tokens' k, v [T, Hkv, d] (bf16 or fp16, k without rotary embedding
+        when the cache has a rope) and separator flags sep [T] uint8 (None: no separators)."""
+        T = _dims(k, 3, "k")[0]
+        for name, t in (("k", k), ("v", v)):
+            _strided(t, (torch.bfloat16, torch.float16), name, (T, self.Hkv, self.d))
+        if k.dtype != v.dtype:
+            raise SepError(f"v has dtype {v.dtype}, k has {k.dtype}")
+        S, max_pages = self._plan(page_table, seq_lens, indptr)
+        if sep is not None:
+            _cuda(sep, torch.uint8, "sep", (T,))
+        self._on_device(("k", k), ("v", v), ("page_table", page_table), ("seq_lens", seq_lens),
+                        ("indptr", indptr), ("sep", sep))
+        if T == 0:
+            return
+        st = self._c()
+        _check(_lib.seppaged_append(ctypes.byref(st), _DTYPES[k.dtype], _ptr(k),
+                                    *self._rows(k, "k"), _ptr(v), *self._rows(v, "v"), _ptr(sep),
+                                    T, S, max_pages, _ptr(page_table), _ptr(seq_lens),
+                                    _ptr(indptr), _stream()), "seppaged_append")
+
+    def seppaged_attn(self, q, page_table, seq_lens, indptr, a=0, n=None, scale=None, out=None,
+                      lse=None, workspace=None):
+        """(O, LSE) of the newest tokens' queries q [T, Hq, d] (bf16 or fp16, rotated) over their
+        sequences' pages: key j is kept iff j <= p and (p - j < n or j < a or flag[j]). n = None
+        keeps every key up to p. Rows that keep nothing: O = 0, LSE = -inf; rows outside
+        indptr's range are left as they are in `out` and `lse`."""
+        T, Hq, d = _dims(q, 3, "q")
+        _strided(q, (torch.bfloat16, torch.float16), "q", (T, Hq, self.d))
+        if Hq < 1 or Hq % self.Hkv != 0:
+            raise SepError(f"Hq = {Hq} is not a multiple of Hkv = {self.Hkv}")
+        S, max_pages = self._plan(page_table, seq_lens, indptr)
+        if S > 4096:
+            raise SepError(f"{S} sequences: at most 4096")
+        if T * Hq > INT32_MAX:
+            raise SepError("more than 2^31 - 1 (token, head) rows")
+        n = INT32_MAX if n is None else int(n)
+        if not 0 <= a <= INT32_MAX or not 0 <= n <= INT32_MAX:
+            raise SepError(f"a = {a} and n = {n} must be between 0 and 2^31 - 1")
+        scale = self.d ** -0.5 if scale is None else scale
+        o = torch.empty(T, Hq, d, dtype=q.dtype, device=q.device) if out is None else out
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
+        _cuda(o, q.dtype, "out", (T, Hq, d))
+        _cuda(lse, torch.float32, "lse", (T, Hq))
+        nbytes = seppaged_attn_workspace_size(S, self.d)
+        ws = _workspace(nbytes, q.device, workspace)
+        self._on_device(("q", q), ("page_table", page_table), ("seq_lens", seq_lens),
+                        ("indptr", indptr), ("out", o), ("lse", lse), ("workspace", ws))
+        if T == 0:
+            return o, lse
+        st = self._c()
+        _check(_lib.seppaged_attn(ctypes.byref(st), _DTYPES[q.dtype], _ptr(q),
+                                  *self._rows(q, "q"), Hq, T, S, max_pages, _ptr(page_table),
+                                  _ptr(seq_lens), _ptr(indptr), int(a), n, float(scale), _ptr(o),
+                                  _ptr(lse), _ptr(ws), ws.numel(), _stream()), "seppaged_attn")
+        return o, lse
+
+
+def seppaged_attn_workspace_size(S, d) -> int:
+    return int(_lib.seppaged_attn_workspace_size(S, d))

@@ -43,3 +43,12 @@ from .sepcache_ref import (  # noqa: F401
     rope_rotate,
     decode_attention,
 )
+from .seppaged_ref import (  # noqa: F401
+    PagedSim,
+    e4m3_decode,
+    e4m3_encode,
+    e4m3_values,
+    page_scale,
+    paged_attend,
+    rope_turn,
+)

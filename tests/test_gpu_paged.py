@@ -1,0 +1,557 @@
+"""The paged e4m3 cache on the GPU: append and attention against the fp64 oracle.
+
+Append. V is stored without arithmetic before its rounding: scales and codes are bit-exact. Keys are
+rotated in fp32 first (within 6e-7 (|x1| + |x2|), the bound of the rotary tests): a code may differ
+from the oracle's only where that moves a value across the middle of two e4m3 numbers, so each stored
+value is held to half an e4m3 step (2^-4 relative, 2^-10 scale below the normals) plus the fp32 bound.
+
+Attention over the stored numbers (the oracle reads the same codes and scales). e4m3 to fp16 and the
+queries' conversion are exact here; a score is a sum of d fp32 products in chains of 16 (error up
+to 2^-19 of sum |q k|); the weights are rounded to fp16: 2^-11 relative, or 2^-25 of the largest weight
+(times a stored number of at most 448 in the scale of its page) in fp16's subnormals; exp2 is within
+2^-21; the output is rounded once. So
+  |o - o*| <= (2^-11 + 4 ds + 2^-19) sum p |v| + N 2^-25 448 max(p vs) + half a step of o,
+  |lse - lse*| <= 2 ds + 2^-20 (1 + |lse|),    ds = 2^-19 max_j scale sum_c |q_c k_jc|.
+"""
+
+import math
+
+import numpy as np
+import pytest
+
+from oracle import seppaged_ref as P
+
+pytestmark = pytest.mark.gpu
+
+SEP_ERR_INDEX = 8
+
+
+@pytest.fixture(scope="module")
+def S():
+    import torch
+    assert torch.cuda.is_available()
+    from kv_cache_compression_sep_b200 import sepattn
+    return sepattn
+
+
+def ints(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def codes(t):
+    import torch
+    return t.view(torch.uint8).cpu().numpy()
+
+
+class Pair:
+    """A cache, its oracle and the page tables of S sequences (pages drawn in random order)."""
+
+    def __init__(self, S_mod, seqs, pages_each, Hkv, d, page, rope=None, seed=0, fill=0x7F):
+        import torch
+        rng = np.random.default_rng(seed)
+        n = seqs * pages_each + 2
+        self.table = rng.permutation(n)[:seqs * pages_each].reshape(seqs, pages_each)
+        self.cache = S_mod.SepPagedCache(n, Hkv, d, page=page, rope=rope)
+        args = () if rope is None else (rope.freq.cpu().numpy(), rope.magnitude, rope.interleaved)
+        self.sim = P.PagedSim(n, Hkv, d, page, *args)
+        # memory that was never written: NaN numbers, a huge scale, set flags
+        for x in "kv":
+            getattr(self.cache, x + "_pages").view(torch.uint8).fill_(fill)
+            getattr(self.cache, x + "_scale").fill_(2.0 ** 40)
+            self.sim.codes[x][:] = fill
+            self.sim.scale[x][:] = 2.0 ** 40
+        self.cache.flags.fill_(1)
+        self.sim.flags[:] = 1
+        self.lens = [0] * seqs
+
+    def append(self, k, v, sep, counts):
+        """counts[s] new tokens for each sequence, from the rows of k, v in order."""
+        ip = np.concatenate([[0], np.cumsum(counts)])
+        self.lens = [l + c for l, c in zip(self.lens, counts)]
+        self.cache.seppaged_append(k, v, ints(self.table.tolist()), ints(self.lens), ints(ip.tolist()), sep=sep)
+        kn, vn = k.double().cpu().numpy(), v.double().cpu().numpy()
+        sn = np.zeros(k.shape[0], dtype=np.uint8) if sep is None else sep.cpu().numpy()
+        for s, c in enumerate(counts):
+            r = slice(ip[s], ip[s + 1])
+            if c:
+                self.sim.append(self.table[s].tolist(), self.lens[s] - c, kn[r], vn[r], sn[r])
+
+    def check(self, key_tol):
+        """V, flags and scales bit-exact, and every byte of memory the oracle leaves alone."""
+        np.testing.assert_array_equal(self.cache.flags.cpu().numpy(), self.sim.flags)
+        np.testing.assert_array_equal(self.cache.v_scale.double().cpu().numpy(), self.sim.scale["v"])
+        np.testing.assert_array_equal(codes(self.cache.v_pages), self.sim.codes["v"])
+        np.testing.assert_array_equal(self.cache.k_scale.double().cpu().numpy(), self.sim.scale["k"])
+        got, want = codes(self.cache.k_pages), self.sim.codes["k"]
+        if key_tol == 0.0:
+            np.testing.assert_array_equal(got, want)
+        else:  # next to each other at most, and only rarely
+            diff = got != want
+            assert diff.mean() <= 1e-3
+            a, b = P.e4m3_decode(got[diff]), P.e4m3_decode(want[diff])
+            assert np.all(np.abs(a - b) <= np.maximum(np.abs(b) * 2.0 ** -3, 2.0 ** -9) * 1.01)
+
+
+def draw(seed, T, H, d, dtype, spread=3):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T, H, d, generator=g, device="cuda")
+    return (x * 2.0 ** torch.randint(-spread, spread + 1, (T, H, 1), generator=g, device="cuda")).to(dtype)
+
+
+APPEND = [
+    # Hkv, d, page, rot, interleaved, dtype, calls of counts
+    (2, 64, 16, 0, False, "bfloat16", [(1, 1), (3, 0), (40, 1), (1, 16), (0, 0, ), (1, 1)]),
+    (8, 128, 64, 128, False, "bfloat16", [(150, 3), (1, 1), (1, 61), (63, 64)]),
+    (3, 64, 32, 24, False, "float16", [(5, 31), (1, 1), (70, 2)]),
+    (1, 128, 128, 64, True, "float16", [(130, 1), (1, 127), (200, 129)]),
+    (5, 64, 128, 64, False, "bfloat16", [(1, 300), (128, 1), (1, 1)]),
+    (12, 64, 16, 32, True, "float16", [(33, 17), (1, 1), (1, 1), (15, 15)]),
+]
+
+
+@pytest.mark.parametrize("Hkv,d,page,rot,inter,dtype,calls", APPEND)
+def test_append(S, Hkv, d, page, rot, inter, dtype, calls):
+    import torch
+    rope = S.sep_rope_table(rot, 10000.0, interleaved=inter) if rot else None
+    most = max(sum(c[s] for c in calls) for s in range(2))
+    pair = Pair(S, 2, -(-most // page), Hkv, d, page, rope, seed=d + page)
+    for i, counts in enumerate(calls):
+        T = sum(counts)
+        k, v = (draw(100 * i + z, T, Hkv, d, getattr(torch, dtype)) for z in (1, 2))
+        sep = (torch.rand(T, device="cuda") < 0.3).to(torch.uint8) if i % 2 else None
+        pair.append(k, v, sep, counts)
+        torch.cuda.synchronize()
+        assert S.sep_last_device_error() == 0
+        pair.check(0.0 if rope is None else 1.0)
+
+
+def test_appended_keys_are_within_half_a_step(S):
+    import torch
+    rope = S.sep_rope_table(128, 500000.0)
+    T, H, d = 333, 4, 128
+    pair = Pair(S, 1, 6, H, d, 64, rope)
+    k, v = draw(5, T, H, d, torch.bfloat16), draw(6, T, H, d, torch.bfloat16)
+    pair.append(k, v, None, (T,))
+    sc = pair.cache.k_scale.double().cpu().numpy()[pair.table[0][np.arange(T) // 64]][:, :, None]
+    num = P.e4m3_decode(codes(pair.cache.k_pages))[pair.table[0][np.arange(T) // 64], :, np.arange(T) % 64]
+    x = k.double().cpu().numpy()
+    ref = P.rope_turn(x, np.arange(T)[:, None], rope.freq.cpu().numpy())
+    size = np.concatenate([np.abs(x[..., :64]) + np.abs(x[..., 64:])] * 2, -1)
+    assert np.all(np.abs(num * sc - ref) <= np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * sc) * 1.0001 + 6e-7 * size)
+    top = np.abs(ref).max()
+    assert np.all(sc * 448.0 >= 0.999 * np.abs(ref)) and np.all(sc * 224.0 <= 1.001 * top)
+
+
+def test_special_values(S):
+    """Zero pages (scale 0), values that are not finite (NaN), tiny and huge ones, a border of the scale."""
+    import torch
+    pair = Pair(S, 1, 4, 2, 64, 16)
+    k = torch.zeros(50, 2, 64, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros_like(k)
+    k[20, 0, 3], k[21, 0, 4], k[22, 1, 5] = math.inf, -math.inf, math.nan
+    k[23, 0, 0], v[23, 0, 0] = 3.5, -3.5          # 448 * 2^-7 exactly
+    k[24, 1, 1], v[24, 1, 1] = 3.515625, 1e-38     # just above; far below the smallest scale's numbers
+    v[33, 0], v[34, 1] = 3.0e38, 1e-36             # one huge row; page 2
+    k[48, 0, 0] = 1e-39                            # a bf16 subnormal alone in its page
+    at = 0
+    for c in (16, 5, 13, 16):
+        pair.append(k[at:at + c], v[at:at + c], None, (c,))
+        at += c
+        torch.cuda.synchronize()
+        pair.check(0.0)
+    assert pair.cache.k_scale[int(pair.table[0][0])].tolist() == [0.0, 0.0]
+
+
+def test_strided_inputs_and_padding(S):
+    """k, v views of a projection; sequences without tokens; rows of the call behind the last sequence
+    and tokens before position 0 are not stored."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    proj = torch.randn(9, 8, 64, generator=g, device="cuda").to(torch.float16)
+    k, v = proj[:, 4:6], proj[:, 6:]
+    pair = Pair(S, 4, 2, 2, 64, 16)
+    table = ints(pair.table.tolist())
+    # sequence 0: 3 tokens; 1: none; 2: 2 tokens of which one stands at -1; 3: none; 4 rows left over
+    pair.cache.seppaged_append(k, v, table, ints([3, 7, 1, 0]), ints([0, 3, 3, 5, 5]))
+    kn, vn = k.double().cpu().numpy(), v.double().cpu().numpy()
+    zero = np.zeros(9, dtype=np.uint8)
+    pair.sim.append(pair.table[0].tolist(), 0, kn[:3], vn[:3], zero)
+    pair.sim.append(pair.table[2].tolist(), 0, kn[4:5], vn[4:5], zero)
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    pair.check(0.0)
+
+
+def test_index_errors_are_reported_and_skipped(S):
+    """Host-side values out of range are caught by the kernels' own checks: nothing is written, the
+    error word says so."""
+    import torch
+    pair = Pair(S, 2, 2, 2, 64, 16)
+    k = torch.ones(4, 2, 64, device="cuda", dtype=torch.bfloat16)
+    q = torch.ones(4, 4, 64, device="cuda", dtype=torch.bfloat16)
+    good = pair.table.tolist()
+    plans = [
+        ([[999, -1], good[1]], [2, 2], [0, 2, 4]),       # pages that do not exist
+        ([[-5, -1], good[1]], [2, 2], [0, 2, 4]),
+        (good, [40, 2], [0, 2, 4]),                      # longer than the table's row
+        (good, [2, 2], [0, 2, 9]),                       # offsets past the call's tokens
+    ]
+    for table, lens, ip in plans:
+        before = codes(pair.cache.k_pages).copy()
+        pair.cache.seppaged_append(k, k, ints(table), ints(lens), ints(ip))
+        assert S.sep_last_device_error() == SEP_ERR_INDEX
+        after = codes(pair.cache.k_pages)
+        changed = np.unique(np.nonzero(after != before)[0])
+        assert set(changed) <= {good[1][0], good[0][0]}
+        pair.cache.seppaged_attn(q, ints(table), ints(lens), ints(ip))
+        assert S.sep_last_device_error() == SEP_ERR_INDEX
+        assert S.sep_last_device_error() == 0
+
+
+# ------------------------------------------------------------------ attention
+def filled(S, seqs, lens, Hkv, d, page, seed, p=0.2, spread=2, extra_pages=0):
+    """A cache holding `lens` tokens of each sequence, appended at once."""
+    import torch
+    pages = max(1, -(-max(lens) // page)) + extra_pages
+    pair = Pair(S, seqs, pages, Hkv, d, page, seed=seed)
+    T = max(1, sum(lens))
+    k, v = draw(seed + 1, T, Hkv, d, torch.bfloat16, spread), draw(seed + 2, T, Hkv, d, torch.bfloat16, spread)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    sep = (torch.rand(T, generator=g, device="cuda") < p).to(torch.uint8)
+    ip = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    pair.cache.seppaged_append(k, v, ints(pair.table.tolist()), ints(lens), ints(ip), sep=sep)
+    pair.lens = list(lens)
+    return pair
+
+
+def sequence(pair, s, length):
+    """Stored values, flags and the largest value scale of one sequence."""
+    page = pair.cache.page
+    ids = pair.table[s][np.arange(length) // page]
+    sl = np.arange(length) % page
+    out = []
+    for x in "kv":
+        num = P.e4m3_decode(codes(getattr(pair.cache, x + "_pages")))[ids, :, sl]
+        out.append(num * getattr(pair.cache, x + "_scale").double().cpu().numpy()[ids][:, :, None])
+    vs = pair.cache.v_scale.double().cpu().numpy()[ids]
+    return out[0], out[1], pair.cache.flags.cpu().numpy()[ids, sl] != 0, vs
+
+
+def check_attn(pair, q, o, lse, counts, a, n, scale, only=None):
+    import torch
+    eps = torch.finfo(o.dtype).eps / 2
+    tiny = torch.finfo(o.dtype).smallest_normal * torch.finfo(o.dtype).eps / 2
+    qn, on, ln = q.double().cpu().numpy(), o.double().cpu().numpy(), lse.double().cpu().numpy()
+    at = 0
+    for s, c in enumerate(counts):
+        r = slice(at, at + c)
+        at += c
+        if c == 0 or (only is not None and s not in only):
+            continue
+        L = pair.lens[s]
+        k, v, flag, vs = sequence(pair, s, L)
+        ro, rl, mag = P.paged_attend(qn[r], k, v, flag, a, n if n is not None else 1 << 40, scale)
+        G = qn.shape[1] // k.shape[1]
+        dot = np.einsum("ihd,jhd->ihj", np.abs(qn[r]), np.abs(np.repeat(k, G, 1))) if L else np.zeros((c, 1, 1))
+        ds = 2.0 ** -19 * scale * dot.max(-1, initial=0.0)
+        # max(p vs) <= the largest scale
+        floor = L * 2.0 ** -25 * 448.0 * (np.repeat(vs, G, 1).max(0, initial=0.0) if L else 0.0)
+        tol = (2.0 ** -11 + 4 * ds + 2.0 ** -19)[:, :, None] * mag + np.asarray(floor)[..., None] + \
+            eps * np.abs(ro) * 1.01 + tiny
+        err = np.abs(on[r] - ro)
+        assert np.all(err <= tol), f"sequence {s}: {np.max(err - tol):.3e} past the bound (max error {err.max():.3e})"
+        dead = np.isneginf(rl)
+        assert np.array_equal(np.isneginf(ln[r]), dead) and np.all(on[r][dead] == 0.0)
+        live = ~dead
+        assert np.all(np.abs(ln[r] - rl)[live] <= (2 * ds + 2.0 ** -20 * (1 + np.abs(rl)))[live])
+
+
+ATTN = [
+    # lens, counts, Hq, Hkv, d, page, dtype, a, n
+    ((1, 2, 3), (1, 1, 1), 4, 2, 64, 16, "bfloat16", 0, None),
+    ((17, 64, 65, 130), (1, 1, 1, 1), 8, 1, 128, 64, "bfloat16", 0, None),
+    ((300, 5, 1000), (1, 1, 1), 32, 8, 128, 64, "bfloat16", 4, 64),
+    ((700, 0, 33), (1, 1, 1), 12, 12, 64, 16, "float16", 2, 16),
+    ((900, 31), (5, 3), 6, 2, 64, 32, "float16", 1, 40),
+    ((200, 77, 513), (7, 2, 1), 7, 1, 128, 128, "bfloat16", 0, None),
+    ((150, 1, 260), (150, 1, 70), 4, 2, 64, 16, "bfloat16", 4, 32),
+    ((90, 600), (9, 300), 4, 4, 128, 64, "float16", 0, None),
+    ((300, 800), (4, 2), 24, 1, 64, 64, "bfloat16", 3, 1),      # more heads in a group than a tile has rows
+    ((620, 2100), (3, 1), 4, 2, 128, 64, "bfloat16", 5, 0),     # no window: initial tokens and separators
+    ((3, 1), (5, 4), 4, 2, 64, 16, "bfloat16", 0, None),        # queries before position 0
+]
+
+
+@pytest.mark.parametrize("lens,counts,Hq,Hkv,d,page,dtype,a,n", ATTN)
+def test_attention(S, lens, counts, Hq, Hkv, d, page, dtype, a, n):
+    import torch
+    pair = filled(S, len(lens), lens, Hkv, d, page, seed=Hq + page)
+    q = draw(77, sum(counts), Hq, d, getattr(torch, dtype), spread=1)
+    ip = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    o, lse = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints(list(lens)), ints(ip), a=a, n=n)
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    check_attn(pair, q, o, lse, counts, a, n, d ** -0.5)
+    # the same bits every time
+    o2, lse2 = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints(list(lens)), ints(ip), a=a, n=n)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dense", [True, False])
+def test_many_sequences_share_the_warps(S, dense):
+    """Runs of tiles that begin and end inside sequences of very different lengths."""
+    import torch
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(0, 70, 130)] + [4000, 1, 0, 2500]
+    counts = [1 if i % 7 else 0 for i in range(len(lens))]
+    pair = filled(S, len(lens), lens, 2, 64, 16, seed=4)
+    q = draw(8, sum(counts), 4, 64, torch.bfloat16)
+    ip = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    a, n = (0, None) if dense else (2, 24)
+    o, lse = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints(lens), ints(ip), a=a, n=n)
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    check_attn(pair, q, o, lse, counts, a, n, 0.125)
+
+
+def test_rows_without_a_key_and_rows_outside(S):
+    """n = 0 without anchors, empty sequences, and output rows that no sequence owns."""
+    import torch
+    pair = filled(S, 3, (40, 30, 0), 2, 64, 16, seed=6, p=0.0)
+    q = draw(3, 8, 4, 64, torch.bfloat16)
+    out = torch.full((8, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, 4), 7.0, device="cuda")
+    plan = (ints(pair.table.tolist()), ints([40, 30, 0]), ints([1, 3, 4, 6]))
+    pair.cache.seppaged_attn(q, *plan, a=0, n=0, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out[1:6] == 0).all() and torch.isneginf(lse[1:6]).all()
+    assert (out[:1] == 7).all() and (out[6:] == 7).all() and (lse[:1] == 7).all() and (lse[6:] == 7).all()
+    pair.cache.seppaged_attn(q, *plan, out=out, lse=lse)
+    check_attn(pair, q[1:6], out[1:6], lse[1:6], (2, 1, 2), 0, None, 0.125)
+
+
+def test_page_scales_far_apart(S):
+    """Value pages whose scales differ by 2^60: the small ones keep their precision where they dominate."""
+    import torch
+    pair = Pair(S, 1, 4, 1, 64, 16)
+    k = draw(1, 64, 1, 64, torch.bfloat16, 0)
+    v = draw(2, 64, 1, 64, torch.bfloat16, 0)
+    v[16:32] *= 2.0 ** 30
+    v[48:] *= 2.0 ** -30
+    v[32:48] = 0.0
+    pair.append(k, v, None, (64,))
+    # the query looks at one key only, in each page in turn: o is that key's value row
+    q = torch.zeros(4, 1, 64, device="cuda", dtype=torch.bfloat16)
+    kk, vv, _, _ = sequence(pair, 0, 64)
+    for i, j in enumerate((3, 20, 40, 50)):
+        q[i, 0] = torch.from_numpy(kk[j, 0] * 40.0 / (kk[j, 0] @ kk[j, 0]) * 8.0 * 8.0).to(torch.bfloat16)
+    for i, j in enumerate((3, 20, 40, 50)):
+        o, lse = pair.cache.seppaged_attn(q[i:i + 1], ints(pair.table.tolist()), ints([64]), ints([0, 1]), scale=1.0)
+        ro, rl, _ = P.paged_attend(q[i:i + 1].double().cpu().numpy(), kk, vv, [False] * 64, 0, 1 << 40, 1.0)
+        on = o.double().cpu().numpy()
+        assert np.all(np.abs(on - ro) <= 0.01 * np.abs(ro).max() + 1e-30)
+        assert abs(float(lse[0, 0]) - rl[0, 0]) <= 0.02
+
+
+@pytest.mark.parametrize("what", ["key", "value"])
+def test_nan_reaches_only_the_rows_that_keep_it(S, what):
+    """A NaN in one token: queries that keep the token see it, the others (earlier, or out of their
+    window) do not, and neither do numbers in slots behind the sequence."""
+    import torch
+    L, c, n = 150, 12, 20
+    pair = filled(S, 1, (L,), 2, 64, 16, seed=9, p=0.0)
+    q = draw(4, c, 4, 64, torch.bfloat16)
+    plan = (ints(pair.table.tolist()), ints([L]), ints([0, c]))
+    clean, clean_lse = pair.cache.seppaged_attn(q, *plan, n=n)
+    j = L - 7                      # tokens L - 12 .. L - 8 do not see it
+    pages = getattr(pair.cache, ("k" if what == "key" else "v") + "_pages").view(torch.uint8)
+    pages[int(pair.table[0][j // 16]), 1, j % 16, 5] = 0xFF
+    jj = L - c - n + 3             # leaves the window of the later queries
+    pages[int(pair.table[0][jj // 16]), 0, jj % 16, 9] = 0x7F
+    o, lse = pair.cache.seppaged_attn(q, *plan, n=n)
+    torch.cuda.synchronize()
+    for i in range(c):
+        p = L - c + i
+        for hq in range(4):
+            t = (j, 5) if hq >= 2 else (jj, 9)
+            keeps = t[0] <= p and p - t[0] < n
+            if not keeps:
+                assert torch.equal(o[i, hq], clean[i, hq]) and torch.equal(lse[i, hq], clean_lse[i, hq])
+            elif what == "key":
+                assert torch.isnan(o[i, hq]).all() and torch.isnan(lse[i, hq])
+            else:
+                assert torch.isnan(o[i, hq, t[1]]) and torch.isnan(o[i, hq]).sum() == 1
+                assert torch.equal(lse[i, hq], clean_lse[i, hq])
+
+
+def test_long_sequence(S):
+    """131071 tokens through the split and the join; a sample of rows against the oracle."""
+    import torch
+    L, Hq, Hkv, d = 131071, 8, 2, 128
+    pair = filled(S, 1, (L,), Hkv, d, 64, seed=21, p=0.1, spread=1)
+    q = draw(5, 2, Hq, d, torch.bfloat16, 0)
+    plan = (ints(pair.table.tolist()), ints([L]), ints([0, 2]))
+    for a, n in ((0, None), (4, 256)):
+        o, lse = pair.cache.seppaged_attn(q, *plan, a=a, n=n)
+        torch.cuda.synchronize()
+        assert S.sep_last_device_error() == 0
+        k, v, flag, vs = sequence(pair, 0, L)
+        for i in range(2):
+            p = L - 2 + i
+            jj = np.arange(L)
+            keep = (jj <= p) & ((p - jj < (n or 1 << 40)) | (jj < a) | flag)
+            for hq in (0, 3, 7):
+                h = hq // 4
+                s = q[i, hq].double().cpu().numpy() @ k[keep, h].T * d ** -0.5
+                w = np.exp(s - s.max())
+                ref = (w / w.sum()) @ v[keep, h]
+                mag = (w / w.sum()) @ np.abs(v[keep, h])
+                floor = keep.sum() * 2.0 ** -25 * 448.0 * (w / w.sum() * vs[keep, h]).max()
+                err = np.abs(o[i, hq].double().cpu().numpy() - ref)
+                assert np.all(err <= 2.0 ** -10 * mag + floor + 2.0 ** -8 * np.abs(ref))
+                assert abs(float(lse[i, hq]) - (s.max() + math.log(w.sum()))) <= 1e-4
+
+
+def test_pool_past_four_gib(S):
+    """Rows of the pool past 2^32 bytes and page numbers near the pool's end."""
+    import torch
+    n = 600_000                                    # 600000 pages * 16 rows * 64 B * 8 heads = 4.9 GB
+    cache = S.SepPagedCache(n, 8, 64, page=16)
+    table = np.array([[n - 1, 3, n - 2, n // 2 + 1]])
+    pair = Pair.__new__(Pair)
+    pair.cache, pair.table, pair.lens = cache, table, [60]
+    k, v = draw(1, 60, 8, 64, torch.bfloat16), draw(2, 60, 8, 64, torch.bfloat16)
+    q = draw(3, 1, 8, 64, torch.bfloat16)
+    plan = (ints(table.tolist()), ints([60]))
+    cache.seppaged_append(k, v, *plan, ints([0, 60]))
+    o, lse = cache.seppaged_attn(q, *plan, ints([0, 1]))
+    torch.cuda.synchronize()
+    ids = table[0][np.arange(60) // 16]
+    sl = np.arange(60) % 16
+    vals = []
+    for x in "kv":
+        pages, scale = getattr(cache, x + "_pages").view(torch.uint8), getattr(cache, x + "_scale")
+        got = P.e4m3_decode(pages[torch.from_numpy(ids).cuda(), :, torch.from_numpy(sl).cuda()].cpu().numpy())
+        vals.append(got * scale[torch.from_numpy(ids).cuda()].double().cpu().numpy()[:, :, None])
+    np.testing.assert_allclose(vals[1], v.double().cpu().numpy(), rtol=2.0 ** -4, atol=1e-2)
+    ro, rl, mag = P.paged_attend(q.double().cpu().numpy(), *vals, np.zeros(60, bool), 0, 1 << 40, 0.125)
+    assert np.all(np.abs(o.double().cpu().numpy() - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -9 * mag)
+
+
+# ------------------------------------------------------------------ together
+def test_decode_in_a_graph_two_streams_shared_prefix(S):
+    """Rotate, append, attend as a server does: a captured step replayed for several tokens, with a
+    workspace of its own, two sequences that share their prefix pages, beside a second cache on another
+    stream; the result is that of eager calls, bit for bit."""
+    import torch
+    rope = S.sep_rope_table(64, 10000.0)
+    H, d, page, steps = 2, 64, 16, 20
+
+    def make():
+        cache = S.SepPagedCache(12, H, d, page=page, rope=rope)
+        table = ints([[0, 1, 2, 3, 4], [0, 1, 5, 6, 7], [8, 9, 10, 11, -1]])
+        k, v = draw(1, 32 + 7, H, d, torch.bfloat16), draw(2, 32 + 7, H, d, torch.bfloat16)
+        # sequences 0 and 1 share 32 tokens; sequence 2 starts with 7
+        cache.seppaged_append(k, v, table[[0, 2]].contiguous(), ints([32, 7]), ints([0, 32, 39]))
+        return cache, table
+
+    qs, ks, vs = (draw(10 + i, steps * 3, h, d, torch.bfloat16).view(steps, 3, h, d) for i, h in enumerate((4, H, H)))
+    start = ints([32, 32, 7])
+
+    def step(cache, table, q, k, v, lens, ip, ws, out, lse):
+        lens.add_(1)
+        qr, _ = S.sep_rope_fwd(q, None, lens - 1, rope)
+        cache.seppaged_append(k, v, table, lens, ip)
+        cache.seppaged_attn(qr, table, lens, ip, a=2, n=12, out=out, lse=lse, workspace=ws)
+
+    ws_bytes = S.seppaged_attn_workspace_size(3, d)
+    ip = ints([0, 1, 2, 3])
+    # eager
+    cache, table = make()
+    lens = start.clone()
+    want = []
+    for i in range(steps):
+        out, lse = torch.empty(3, 4, d, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 4, device="cuda")
+        step(cache, table, qs[i], ks[i], vs[i], lens, ip, None, out, lse)
+        want.append((out, lse))
+    torch.cuda.synchronize()
+    # captured, twice, replayed side by side on two streams
+    runs = []
+    for _ in range(2):
+        cache2, table2 = make()
+        st = dict(cache=cache2, lens=start.clone(), q=qs[0].clone(), k=ks[0].clone(), v=vs[0].clone(),
+                  ws=torch.empty(ws_bytes, dtype=torch.uint8, device="cuda"), got=[],
+                  out=torch.empty(3, 4, d, dtype=torch.bfloat16, device="cuda"), lse=torch.empty(3, 4, device="cuda"),
+                  stream=torch.cuda.Stream(), graph=torch.cuda.CUDAGraph())
+        torch.cuda.synchronize()
+        with torch.cuda.graph(st["graph"]):
+            step(cache2, table2, st["q"], st["k"], st["v"], st["lens"], ip, st["ws"], st["out"], st["lse"])
+        st["table"] = table2
+        runs.append(st)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        for st in runs:
+            with torch.cuda.stream(st["stream"]):
+                for x, y in (("q", qs), ("k", ks), ("v", vs)):
+                    st[x].copy_(y[i])
+                st["graph"].replay()
+                st["got"].append((st["out"].clone(), st["lse"].clone()))
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    for st in runs:
+        for (o, l), (wo, wl) in zip(st["got"], want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+        assert torch.equal(st["cache"].k_pages.view(torch.uint8), cache.k_pages.view(torch.uint8))
+
+
+def test_prompt_in_chunks_equals_the_separator_attention(S):
+    """A prompt rotated and appended chunk by chunk, each chunk attending to its past, against
+    sep_attn_fwd over the same (stored) keys and values in bf16: the e4m3 numbers times a power of two are
+    bf16 numbers, so the two see the same inputs."""
+    import torch
+    L, Hq, Hkv, d, a, n = 333, 4, 2, 64, 4, 64
+    rope = S.sep_rope_table(d, 10000.0)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    q, k, v = (torch.randn(L, h, d, generator=g, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    sep = (torch.rand(L, generator=g, device="cuda") < 0.15).to(torch.uint8)
+    pair = Pair(S, 1, 11, Hkv, d, 32, rope)
+    table = ints(pair.table.tolist())
+    pos = torch.arange(L, device="cuda")
+    qr, _ = S.sep_rope_fwd(q, None, pos, rope)
+    outs = []
+    at = 0
+    chunks = (100, 1, 64, 120, 48)
+    for c in chunks:
+        lens, ip = ints([at + c]), ints([0, c])
+        pair.cache.seppaged_append(k[at:at + c], v[at:at + c], table, lens, ip, sep=sep[at:at + c])
+        outs.append(pair.cache.seppaged_attn(qr[at:at + c], table, lens, ip, a=a, n=n))
+        at += c
+    # the pages' scales only grew inside a page, so the last state holds every row as it was, unless a
+    # page was re-expressed: append the prompt at once for the reference's keys
+    one = Pair(S, 1, 11, Hkv, d, 32, rope)
+    one.append(k, v, sep, (L,))
+    kk, vv, _, _ = sequence(one, 0, L)
+    kb, vb = (torch.from_numpy(x).cuda().to(torch.bfloat16)[None] for x in (kk, vv))
+    mask = S.sep_mask_build(sep[None], a, n)
+    ro, rl = S.sep_attn_fwd(qr[None], kb.contiguous(), vb.contiguous(), mask)
+    o, lse = torch.cat([x[0] for x in outs]), torch.cat([x[1] for x in outs])
+    # forward: bf16 weights (2^-8) and output; here fp16 weights; a re-expressed number moves by at most
+    # 2^-10 of its page's scale
+    assert (o.float() - ro[0].float()).abs().max() <= 2e-2
+    assert (lse - rl[0].T).abs().max() <= 4e-3
+
+
+def test_checkpoint(S):
+    import torch
+    pair = filled(S, 2, (50, 20), 2, 64, 16, seed=2)
+    sd = pair.cache.state_dict()
+    other = S.SepPagedCache(pair.cache.num_pages, 2, 64, page=16)
+    other.load_state_dict(sd)
+    q = draw(4, 2, 4, 64, torch.float16)
+    plan = (ints(pair.table.tolist()), ints([50, 20]), ints([0, 1, 2]))
+    for x, y in zip(other.seppaged_attn(q, *plan), pair.cache.seppaged_attn(q, *plan)):
+        assert torch.equal(x, y)
+    with pytest.raises(S.SepError, match="load_state_dict"):
+        S.SepPagedCache(3, 2, 64, page=16).load_state_dict(sd)

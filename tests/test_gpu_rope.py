@@ -1,0 +1,182 @@
+"""sep_rope_fwd / sep_rope_bwd against the fp64 oracle.
+
+Bound per element. cos and sin: the reduced angle is rounded to fp32 (pi 2^-24 at most) and sincosf
+is within 2 ulp (2^-23 for values up to 1, twice), and the magnitude and the products add a rounding
+each: 6e-7 m (|x1| + |x2|) in all. The result is rounded once to its type: half a step relative to it,
+or half the smallest subnormal.
+"""
+
+import numpy as np
+import pytest
+
+from gpu_common import f64
+from oracle import seppaged_ref as P
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def S():
+    import torch
+    assert torch.cuda.is_available()
+    from kv_cache_compression_sep_b200 import sepattn
+    return sepattn
+
+
+def check(y, x, pos, rope, inverse, extra=0.0):
+    """pos broadcast on x's leading axes (without heads)."""
+    import torch
+    xf = x.detach().double().cpu().numpy()
+    ref = P.rope_turn(xf, pos[..., None], rope.freq.cpu().numpy(), rope.magnitude, rope.interleaved, inverse)
+    h = rope.d_rot // 2
+    one = np.arange(h)
+    i1, i2 = (2 * one, 2 * one + 1) if rope.interleaved else (one, one + h)
+    size = np.zeros(x.shape)
+    size[..., i1] = size[..., i2] = np.abs(xf[..., i1]) + np.abs(xf[..., i2])
+    fin = torch.finfo(x.dtype)
+    tol = (6e-7 + extra) * abs(rope.magnitude) * size + fin.eps / 2 * np.abs(ref) * 1.0001 + fin.smallest_normal * fin.eps / 2
+    err = np.abs(y.detach().double().cpu().numpy() - ref)
+    assert np.all(err <= tol), f"{np.max(err - tol):.3e} past the bound"
+    assert np.array_equal(f64(y)[..., rope.d_rot:], f64(x)[..., rope.d_rot:])
+
+
+CASES = [
+    # dtype, lead, Hq, Hkv, d, rot, interleaved, scaling
+    ("bfloat16", (1,), 4, 2, 64, 64, False, None),
+    ("bfloat16", (2, 37), 12, 12, 64, 16, False, None),
+    ("float16", (3, 50), 7, 1, 128, 128, True, dict(type="yarn", factor=16.0, original_max_position=4096)),
+    ("bfloat16", (700,), 32, 8, 128, 128, False,
+     dict(type="llama3", factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0, original_max_position=8192)),
+    ("float32", (2, 33), 3, 2, 64, 24, False, dict(type="linear", factor=4.0)),   # halves of 12 elements
+    ("float16", (1, 19), 5, 5, 80, 24, False, dict(type="ntk", factor=4.0)),      # unaligned halves
+    ("bfloat16", (2, 9), 3, 1, 66, 10, True, None),                               # unaligned rows
+    ("float32", (41,), 2, 1, 6, 2, False, None),
+    ("bfloat16", (1, 5000), 4, 1, 256, 256, False, None),                         # many tokens per CTA
+]
+
+
+@pytest.mark.parametrize("dtype,lead,Hq,Hkv,d,rot,inter,scaling", CASES)
+@pytest.mark.parametrize("pos64,backward", [(False, False), (True, True)])
+def test_values(S, dtype, lead, Hq, Hkv, d, rot, inter, scaling, pos64, backward):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(d + rot)
+    t = getattr(torch, dtype)
+    rope = S.sep_rope_table(rot, 10000.0, interleaved=inter, scaling=scaling)
+    q, k = (torch.randn(*lead, h, d, generator=g, device="cuda").to(t) for h in (Hq, Hkv))
+    pos = torch.randint(-100, 200000, lead, generator=g, device="cuda", dtype=torch.int64 if pos64 else torch.int32)
+    q0, k0 = q.clone(), k.clone()
+    fn = S.sep_rope_bwd if backward else S.sep_rope_fwd
+    yq, yk = fn(q, k, pos, rope)
+    torch.cuda.synchronize()
+    assert torch.equal(q, q0) and torch.equal(k, k0)
+    check(yq, q, pos.cpu().numpy(), rope, backward)
+    check(yk, k, pos.cpu().numpy(), rope, backward)
+    # in place: the same bits
+    out = fn(q, k, pos, rope, out=(q, k))
+    torch.cuda.synchronize()
+    assert out[0] is q and torch.equal(q, yq) and torch.equal(k, yk)
+    # q alone
+    assert torch.equal(fn(q0, None, pos, rope)[0], yq)
+
+
+@pytest.mark.parametrize("inter,rot", [(False, 64), (True, 64), (False, 24), (True, 12)])
+def test_views_of_a_projection_in_place_and_shared_positions(S, inter, rot):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(rot)
+    B, L, Hq, Hkv, d = 3, 45, 4, 2, 64
+    proj = torch.randn(B, L, (Hq + 2 * Hkv) * d + 8, generator=g, device="cuda").to(torch.bfloat16)
+    before = proj.clone()
+    q = proj[..., :Hq * d].unflatten(-1, (Hq, d))
+    k = proj[..., Hq * d:(Hq + Hkv) * d].unflatten(-1, (Hkv, d))
+    rope = S.sep_rope_table(rot, 500.0, interleaved=inter)
+    pos = torch.arange(L, device="cuda") * 3
+    yq, yk = S.sep_rope_fwd(q, k, pos, rope)
+    pn = np.broadcast_to(pos.cpu().numpy(), (B, L))
+    check(yq, q, pn, rope, False)
+    check(yk, k, pn, rope, False)
+    S.sep_rope_fwd(q, k, pos, rope, out=(q, k))
+    torch.cuda.synchronize()
+    assert torch.equal(q, yq) and torch.equal(k, yk)
+    tail = slice((Hq + Hkv) * d, None)
+    assert torch.equal(proj[..., tail], before[..., tail])  # values and padding of the projection
+
+
+def test_transposed_and_expanded_inputs(S):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q = torch.randn(2, 6, 31, 64, generator=g, device="cuda").to(torch.float16).transpose(1, 2)
+    k = torch.randn(2, 31, 1, 64, generator=g, device="cuda").to(torch.float16).expand(2, 31, 3, 64)
+    pos = torch.randint(0, 999, (2, 31), generator=g, device="cuda")
+    rope = S.sep_rope_table(64, 10000.0)
+    yq, yk = S.sep_rope_fwd(q, k, pos, rope)
+    check(yq, q, pos.cpu().numpy(), rope, False)
+    check(yk, k, pos.cpu().numpy(), rope, False)
+    with pytest.raises(S.SepError, match="expanded"):
+        S.sep_rope_fwd(q, k, pos, rope, out=(yq, k))
+    with pytest.raises(S.SepError, match="overlaps"):
+        buf = torch.zeros(2, 32, 6, 64, device="cuda", dtype=torch.float16)
+        S.sep_rope_fwd(buf[:, :31], None, pos, rope, out=(buf[:, 1:],))
+
+
+def test_far_positions_and_rows_past_two_gib(S):
+    """Positions near 2^27 (their fp64 angle carries 2^27 * 2^-52), and a tensor whose last rows start
+    past 2^31 elements."""
+    import torch
+    rope = S.sep_rope_table(64, 10000.0)
+    big = torch.zeros(140000, 240, 64, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(10)
+    big[-40:] = torch.randn(40, 240, 64, generator=g, device="cuda").to(torch.bfloat16)
+    x = big[-40:].clone()
+    pos = torch.arange(140000, device="cuda", dtype=torch.int32) + (1 << 27)
+    S.sep_rope_fwd(big, None, pos, rope, out=(big,))
+    check(big[-40:], x, pos[-40:].cpu().numpy(), rope, False, extra=6e-8)
+    assert not big[:-40].any()
+
+
+def test_backward_is_the_gradient(S):
+    """<R x, g> = <x, R' g> in fp32, and R' undoes R up to magnitude^2."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rope = S.sep_rope_table(96, 10000.0, interleaved=True,
+                            scaling=dict(type="yarn", factor=4.0, original_max_position=128))
+    x, dy = (torch.randn(2, 70, 3, 128, generator=g, device="cuda") for _ in range(2))
+    pos = torch.randint(0, 400, (2, 70), generator=g, device="cuda")
+    y, _ = S.sep_rope_fwd(x, None, pos, rope)
+    dx, _ = S.sep_rope_bwd(dy, None, pos, rope)
+    lhs, rhs = (y.double() * dy.double()).sum(), (x.double() * dx.double()).sum()
+    scale = (y.double() * dy.double()).abs().sum()
+    assert abs(lhs - rhs) <= 2e-6 * scale
+    back, _ = S.sep_rope_bwd(y, None, pos, rope)
+    m2 = rope.magnitude ** 2
+    assert (back[..., :96] - m2 * x[..., :96]).abs().max() <= 2e-5
+    # one coordinate by differences (the map is linear: the difference is exact up to rounding)
+    for at in ((0, 5, 1, 7), (1, 69, 2, 94), (0, 0, 0, 100)):
+        e = torch.zeros_like(x)
+        e[at] = 1.0
+        ye, _ = S.sep_rope_fwd(e, None, pos, rope)
+        assert abs((ye.double() * dy.double()).sum() - dx[at].double()) <= 1e-5
+
+
+def test_graph_stream_and_empty(S):
+    import torch
+    rope = S.sep_rope_table(64, 10000.0)
+    q = torch.randn(4, 8, 64, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(4, device="cuda")
+    out = torch.empty_like(q)
+    S.sep_rope_fwd(q, None, pos, rope, out=(out,))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.sep_rope_fwd(q, None, pos, rope, out=(out,))
+    q.copy_(torch.randn(4, 8, 64, device="cuda"))
+    pos.add_(1000)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(out, q, pos.cpu().numpy(), rope, False)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        y, _ = S.sep_rope_fwd(q, None, pos, rope)
+    side.synchronize()
+    assert torch.equal(y, out)
+    e, _ = S.sep_rope_fwd(q[:0], None, pos[:0], rope)
+    assert e.shape == (0, 8, 64)

@@ -1,0 +1,265 @@
+"""Argument checks of the rotary and paged-cache calls, and the frequency table (CPU only)."""
+
+import ctypes
+import math
+import types
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_compression_sep_b200 import sepattn as S
+
+INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 1, 2, 3, 6
+P16 = 4096  # an address that is never read
+
+
+# ------------------------------------------------------------------ frequencies
+def test_frequencies_plain_linear_ntk():
+    w, m = S._scaled_frequencies(64, 10000.0, None)
+    assert m == 1.0
+    np.testing.assert_allclose(w, 10000.0 ** (-2.0 * np.arange(32) / 64), rtol=1e-14)
+    lin, _ = S._scaled_frequencies(64, 10000.0, dict(type="linear", factor=4.0))
+    np.testing.assert_allclose(np.array(lin) * 4.0, w, rtol=1e-15)
+    ntk, _ = S._scaled_frequencies(64, 10000.0, dict(type="ntk", factor=4.0))
+    # the highest frequency stays, the lowest is divided by the factor
+    assert ntk[0] == 1.0 and ntk[-1] * 4.0 == pytest.approx(w[-1], rel=1e-12)
+
+
+def test_frequencies_llama3():
+    opt = dict(type="llama3", factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0,
+               original_max_position=8192)
+    w, _ = S._scaled_frequencies(128, 500000.0, None)
+    got, m = S._scaled_frequencies(128, 500000.0, opt)
+    assert m == 1.0
+    for x, y in zip(w, got):
+        wave = 2.0 * math.pi / x
+        if wave < 8192 / 4.0:
+            assert y == x
+        elif wave > 8192:
+            assert y == pytest.approx(x / 8.0, rel=1e-15)
+        else:
+            assert x / 8.0 < y < x
+    assert sorted(got, reverse=True) == got
+
+
+def test_frequencies_yarn():
+    opt = dict(type="yarn", factor=16.0, original_max_position=4096)
+    w, _ = S._scaled_frequencies(128, 10000.0, None)
+    got, m = S._scaled_frequencies(128, 10000.0, opt)
+    assert m == pytest.approx(0.1 * math.log(16.0) + 1.0)
+    for x, y in zip(w, got):
+        turns = 4096 * x / (2.0 * math.pi)
+        if turns > 40.0:
+            assert y == x
+        elif turns < 0.8:
+            assert y == pytest.approx(x / 16.0, rel=1e-15)
+    assert S._scaled_frequencies(128, 1e4, dict(opt, attention_factor=0.7))[1] == 0.7
+
+
+@pytest.mark.parametrize("scaling,match", [
+    (dict(type="other", factor=2.0), "scaling type"),
+    (dict(type="linear"), "needs"),
+    (dict(type="linear", factor=0.5), "at least 1"),
+    (dict(type="linear", factor=2.0, beta_fast=1.0), "unknown"),
+    (dict(type="llama3", factor=8.0, low_freq_factor=4.0, high_freq_factor=1.0,
+          original_max_position=8192), "low_freq_factor"),
+    (dict(type="yarn", factor=8.0, original_max_position=4096, beta_fast=1.0, beta_slow=2.0), "beta"),
+    (dict(type="yarn", factor=8.0, original_max_position=0), "positive"),
+])
+def test_frequency_refusals(scaling, match):
+    with pytest.raises(S.SepError, match=match):
+        S.sep_rope_table(64, 10000.0, scaling=scaling)
+
+
+def test_table_refusals():
+    for bad in (0, 3, -2):
+        with pytest.raises(S.SepError, match="d_rot"):
+            S.sep_rope_table(bad, 10000.0)
+    with pytest.raises(S.SepError, match="theta"):
+        S.sep_rope_table(64, 0.0)
+    with pytest.raises(S.SepError, match="CUDA"):
+        S.sep_rope_table(64, 10000.0, device="cpu")
+
+
+# ------------------------------------------------------------------ binding
+def _rope(d_rot=64):
+    return S.SepRope(torch.zeros(d_rot // 2, dtype=torch.float64), d_rot, False, 1.0)
+
+
+def test_rope_binding_refusals():
+    q = torch.zeros(2, 5, 4, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(2, 5, dtype=torch.int32)
+    for call in (S.sep_rope_fwd, S.sep_rope_bwd):
+        with pytest.raises(S.SepError, match="CUDA"):
+            call(q, q, pos, _rope())
+        with pytest.raises(S.SepError, match="sep_rope_table"):
+            call(q, q, pos, None)
+        with pytest.raises(S.SepError, match="larger"):
+            call(q, q, pos, _rope(128))
+        with pytest.raises(S.SepError, match="tokens, heads, d"):
+            call(q[0, 0], None, pos, _rope())
+
+
+def test_address_ranges_of_views():
+    buf = torch.zeros(2, 5, 12, 64)
+    q, k, v = buf[:, :, :8], buf[:, :, 8:10], buf[:, :, 10:]
+    assert S._overlap(q, q) and S._overlap(q, buf[:, :, 4:])
+    assert not S._overlap(k, v) and not S._overlap(v, k)
+    assert not S._overlap(q, torch.zeros(4))
+    assert S._overlap(buf[:, :4], buf[:, 1:])
+
+
+class FakeCuda(torch.Tensor):
+    """A CPU tensor that says it is on the GPU: the checks past the device ones, never a launch."""
+
+    @staticmethod
+    def __new__(cls, t):
+        return torch.Tensor._make_subclass(cls, t)
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def _paged(monkeypatch, **kw):
+    """A SepPagedCache whose tensors live on the CPU and whose library calls must not be reached."""
+    opt = dict(num_pages=6, Hkv=2, d=64, page=16, rope=None)
+    opt.update(kw)
+    c = S.SepPagedCache.__new__(S.SepPagedCache)
+    c.__dict__.update(opt)
+    shape = (opt["num_pages"], opt["Hkv"], opt["page"], opt["d"])
+    f = lambda t: FakeCuda(t)  # noqa: E731
+    c.k_pages = f(torch.zeros(shape, dtype=torch.uint8).view(torch.float8_e4m3fn))
+    c.v_pages = f(torch.zeros(shape, dtype=torch.uint8).view(torch.float8_e4m3fn))
+    c.k_scale, c.v_scale = f(torch.zeros(shape[:2])), f(torch.zeros(shape[:2]))
+    c.flags = f(torch.zeros(shape[0], shape[2], dtype=torch.uint8))
+    never = types.SimpleNamespace(seppaged_append=None, seppaged_attn=None,
+                                  seppaged_attn_workspace_size=lambda S_, d: 256)
+    monkeypatch.setattr(S, "_lib", never)
+    return c
+
+
+def _plan(S_=3, pages=2):
+    f = FakeCuda
+    return (f(torch.zeros(S_, pages, dtype=torch.int32)), f(torch.zeros(S_, dtype=torch.int32)),
+            f(torch.zeros(S_ + 1, dtype=torch.int32)))
+
+
+def test_paged_constructor_refusals():
+    for kw, match in ((dict(d=96), "head dimension"), (dict(page=24), "page size"),
+                      (dict(num_pages=0), "positive"), (dict(num_pages=1 << 27), "2\\^32"),
+                      (dict(rope=3), "sep_rope_table"), (dict(rope=_rope(128)), "larger"),
+                      (dict(device="cpu"), "CUDA")):
+        args = dict(num_pages=4, Hkv=2, d=64)
+        args.update(kw)
+        with pytest.raises(S.SepError, match=match):
+            S.SepPagedCache(**args)
+
+
+def test_append_binding_refusals(monkeypatch):
+    c = _paged(monkeypatch)
+    k = FakeCuda(torch.zeros(3, 2, 64, dtype=torch.bfloat16))
+    table, lens, ip = _plan()
+
+    def refuses(match, k_=k, v_=k, plan=(table, lens, ip), sep=None):
+        with pytest.raises(S.SepError, match=match):
+            c.seppaged_append(k_, v_, *plan, sep=sep)
+
+    refuses("3-D", k_=k[0])
+    refuses("dtype", k_=FakeCuda(torch.zeros(3, 2, 64)), v_=k)
+    refuses("shape", v_=FakeCuda(torch.zeros(2, 2, 64, dtype=torch.bfloat16)))
+    refuses("dtype", v_=FakeCuda(torch.zeros(3, 2, 64, dtype=torch.float16)))
+    refuses("last dimension", k_=FakeCuda(torch.zeros(3, 2, 128, dtype=torch.bfloat16))[:, :, ::2])
+    refuses("page_table", plan=(lens, lens, ip))
+    refuses("seq_lens", plan=(table, ip, ip))
+    refuses("indptr", plan=(table, lens, lens))
+    refuses("dtype", plan=(FakeCuda(table.long()), lens, ip))
+    refuses("sep", sep=FakeCuda(torch.zeros(4, dtype=torch.uint8)))
+    refuses("CUDA", k_=torch.zeros(3, 2, 64, dtype=torch.bfloat16))
+
+
+def test_attn_binding_refusals(monkeypatch):
+    c = _paged(monkeypatch)
+    q = FakeCuda(torch.zeros(3, 4, 64, dtype=torch.bfloat16))
+    plan = _plan()
+
+    def refuses(match, q_=q, plan_=plan, **kw):
+        with pytest.raises(S.SepError, match=match):
+            c.seppaged_attn(q_, *plan_, **kw)
+
+    refuses("multiple", q_=FakeCuda(torch.zeros(3, 3, 64, dtype=torch.bfloat16)))
+    refuses("shape", q_=FakeCuda(torch.zeros(3, 4, 128, dtype=torch.bfloat16)))
+    refuses("dtype", q_=FakeCuda(torch.zeros(3, 4, 64)))
+    refuses("between", a=-1)
+    refuses("between", n=-1)
+    refuses("at most 4096", plan_=_plan(4097))
+    refuses("out has dtype", out=FakeCuda(torch.zeros(3, 4, 64)))
+    refuses("lse has shape", out=q, lse=FakeCuda(torch.zeros(4, 3)))
+
+
+# ------------------------------------------------------------------ C entry points
+class _State(ctypes.Structure):
+    _fields_ = S._SepPagedState._fields_
+
+
+def _state(**kw):
+    base = dict(num_pages=4, Hkv=2, d=64, page=16, k_pages=P16, v_pages=P16, k_scale=P16, v_scale=P16,
+                flags=P16, rope=S._SepRope(None, 0, 0, 1.0))
+    base.update(kw)
+    return S._SepPagedState(**base)
+
+
+def _append(st=None, dtype=0, k=P16, ktok=128, khead=64, T=3, S_=2, mp=2, table=P16, lens=P16, ip=P16):
+    return S._lib.seppaged_append(ctypes.byref(st or _state()), dtype, k, ktok, khead, P16, 128, 64, None,
+                                  T, S_, mp, table, lens, ip, None)
+
+
+def test_append_entry_refusals():
+    assert _append(st=_state(k_pages=None)) == INVALID
+    assert _append(st=_state(num_pages=0)) == INVALID
+    assert _append(k=None) == INVALID and _append(table=None) == INVALID
+    assert _append(T=0) == INVALID and _append(S_=0) == INVALID and _append(mp=0) == INVALID
+    assert _append(st=_state(d=96)) == UNSUPPORTED
+    assert _append(st=_state(page=48)) == UNSUPPORTED
+    assert _append(st=_state(num_pages=1 << 30)) == UNSUPPORTED
+    assert _append(dtype=2) == UNSUPPORTED and _append(dtype=7) == UNSUPPORTED
+    assert _append(k=P16 + 8) == MISALIGNED and _append(ktok=132) == MISALIGNED
+    assert _append(st=_state(v_pages=P16 + 8)) == MISALIGNED
+    assert _append(st=_state(rope=S._SepRope(P16, 66, 0, 1.0))) == INVALID
+    assert _append(st=_state(rope=S._SepRope(P16, 7, 0, 1.0))) == INVALID
+    assert _append(st=_state(rope=S._SepRope(None, 64, 0, 1.0))) == INVALID
+
+
+def _attn(st=None, dtype=0, q=P16, Hq=4, T=3, S_=2, a=0, n=8, o=P16, ws=P16, nbytes=1 << 40):
+    return S._lib.seppaged_attn(ctypes.byref(st or _state()), dtype, q, 256, 64, Hq, T, S_, 2, P16, P16, P16,
+                                a, n, 1.0, o, P16, ws, nbytes, None)
+
+
+def test_attn_entry_refusals():
+    assert _attn(Hq=3) == INVALID and _attn(a=-1) == INVALID and _attn(n=-1) == INVALID
+    assert _attn(q=None) == INVALID and _attn(o=None) == INVALID
+    assert _attn(S_=4097) == UNSUPPORTED and _attn(T=1 << 30) == UNSUPPORTED
+    assert _attn(dtype=2) == UNSUPPORTED
+    assert _attn(q=P16 + 8) == MISALIGNED and _attn(o=P16 + 2) == MISALIGNED
+    assert _attn(ws=P16 + 16) == MISALIGNED
+    assert _attn(ws=None) == WORKSPACE
+    assert _attn(nbytes=S.seppaged_attn_workspace_size(2, 64) - 1) == WORKSPACE
+    assert S.seppaged_attn_workspace_size(0, 64) == 0
+
+
+def test_rope_entry_refusals():
+    def call(fn=S._lib.sep_rope_fwd, rope=(P16, 64, 0, 1.0), dtype=0, B=1, L=4, d=64, pos=P16, pos64=0, x=P16,
+             H=2):
+        r = S._SepRope(*rope)
+        t = S._SepRopeTensor(x, P16, (ctypes.c_int64 * 3)(0, 128, 64), (ctypes.c_int64 * 3)(0, 128, 64), H)
+        return fn(ctypes.byref(r), dtype, B, L, d, pos, pos64, 0, ctypes.byref(t), None, None)
+
+    for fn in (S._lib.sep_rope_fwd, S._lib.sep_rope_bwd):
+        assert call(fn, rope=(None, 64, 0, 1.0)) == INVALID
+        assert call(fn, rope=(P16, 66, 0, 1.0)) == INVALID
+        assert call(fn, rope=(P16, 5, 0, 1.0)) == INVALID
+        assert call(fn, B=0) == INVALID and call(fn, H=0) == INVALID and call(fn, x=None) == INVALID
+        assert call(fn, dtype=3) == UNSUPPORTED and call(fn, d=640) == UNSUPPORTED
+        assert call(fn, B=1 << 20, L=1 << 20) == UNSUPPORTED
+        assert call(fn, x=P16 + 1) == MISALIGNED and call(fn, pos=P16 + 4, pos64=1) == MISALIGNED
