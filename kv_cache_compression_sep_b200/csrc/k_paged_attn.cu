@@ -11,10 +11,10 @@
 //
 // The stored numbers are read once from HBM and that bounds the call (2 d bytes per key and KV
 // head, 4 d flops per query head). One warp is the unit of work: it takes 8 NT query rows (the
-// group's heads of one or more tokens) against a run of keys, its keys and values go from global
-// memory straight into the fragments of mma.sync (S^T = K Q^T and O^T = V^T P^T, keys or value
-// columns on the 16-row side, so that 8 query rows fill the 8-column side), and nothing in the
-// main loop waits for another warp. e4m3 -> fp16 is exact; queries enter as fp16 scaled per row
+// group's heads of one or more tokens) against a run of keys, copies them through a ring of its own in
+// shared memory (cp.async, 32 keys a stage) into the fragments of mma.sync (S^T = K Q^T and O^T =
+// V^T P^T, keys or value columns on the 16-row side, so that 8 query rows fill the 8-column side),
+// and nothing in the main loop waits for another warp. e4m3 -> fp16 is exact; queries enter as fp16 scaled per row
 // by a power of two (bf16 has fewer significant bits, so that is exact above 2^-28 of the row's
 // largest); the weights are rounded to fp16 (2^-11); sums are fp32. The tensor cores are far from
 // busy here (a query group of 8 rows uses 2 x 8 x 16 x 16 products per 16 keys and 16 columns), so
@@ -41,7 +41,10 @@ namespace sep {
 namespace {
 
 constexpr int kWarps = 4;            // per CTA
-constexpr int kScan = 512;           // positions of a tile left of the window (kept rows are gathered)
+// CTAs per SM. With two, a warp keeps its state in registers and 64 x 8192 tokens take 148 us; three (12
+// warps, 168 registers, a few spills) take 161 us.
+constexpr int kCtasPerSm = 2;
+constexpr int kScan = 256;           // positions of a tile left of the window (kept rows are gathered)
 constexpr int kDense = 64;           // positions of a window tile (every row loaded)
 constexpr int kMaxWarps = 2048;      // workspace slots are laid out for this many
 
@@ -143,59 +146,88 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 
 constexpr uint32_t kNoRow = 0xffffffffu;
 
-// log2 of a page's scale: a power of two, or 0 while the page holds only zeros
-__device__ __forceinline__ float log2_of_scale(float s) {
-  return s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : -INFINITY;
+// The exponent fields of a page's scales (powers of two, or 0 while the page holds only zeros), and the
+// key scale and the log2 of the value scale (-inf for 0) from them.
+__device__ __forceinline__ uint32_t scale_exponents(float ks, float vs) {
+  return (__float_as_uint(ks) >> 23 & 0xffu) | (__float_as_uint(vs) >> 23 & 0xffu) << 8;
+}
+__device__ __forceinline__ float key_scale(uint32_t ex) { return __uint_as_float((ex & 0xffu) << 23); }
+__device__ __forceinline__ float value_log2(uint32_t ex) {
+  return ex >> 8 ? (float)((int)(ex >> 8) - 127) : -INFINITY;
 }
 
-// Keys and values of 32 positions in fragment order. Lane (g = lane / 4, t = lane % 4):
-// K: key 16 i + 8 u + g, elements 16 t .. 16 t + 15 of each 64; V: keys 16 i + 2 t + {0, 1, 8, 9},
-// columns (D / 8) g ..
+// A stage of a warp's ring: 32 key rows, then 32 value rows, D bytes each, in 16-byte pieces. Piece c of
+// row r lies at piece c ^ swz(r), so that the fragment reads (several rows at one piece) and the copies
+// (whole rows) both touch every bank once (D = 64: values twice).
 template <int D>
-struct KFrag {
-  uint4 x[2][2][D / 64];
+struct Ring {
+  static constexpr int kRows = 32, kBytes = 2 * kRows * D, kStages = 2, kPieces = D / 16;
+  static __device__ __forceinline__ uint32_t at(int row, int piece) {
+    return (uint32_t)(row * D + ((piece ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+  }
 };
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
+  // a size of 0 reads nothing and fills with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Copies the rows of a stage; row_of(r, &on) is the pool row of stage row r.
+template <int D, typename RowOf>
+__device__ __forceinline__ void fetch32(const PagedAttnParams& p, uint32_t stage, int lane, RowOf row_of) {
+  using C = Ring<D>;
+  constexpr int kPerCopy = 32 / C::kPieces;  // rows per warp-wide copy
+  const int piece = lane % C::kPieces;
+#pragma unroll
+  for (int j = 0; j < C::kRows / kPerCopy; ++j) {
+    const int r = j * kPerCopy + lane / C::kPieces;
+    bool on;
+    const uint32_t row = row_of(r, &on);
+    const size_t off = on ? (size_t)row * D + piece * 16 : 0;
+    copy16(stage + C::at(r, piece), p.k_pages + off, on);
+    copy16(stage + C::kRows * D + C::at(r, piece), p.v_pages + off, on);
+  }
+  copy_commit();
+}
+
+// Values of 16 keys in fragment order: lane (g = lane / 4, t = lane % 4) has columns (D / 8) g .. of
+// keys 2 t + {0, 1, 8, 9}.
 template <int D>
 struct VFrag {
-  uint32_t x[2][4][D / 32];
+  uint32_t x[4][D / 32];
 };
-
 template <int D>
-__device__ __forceinline__ void load_k(KFrag<D>& f, const uint8_t* base, const uint32_t (&row)[2][2], int t) {
+__device__ __forceinline__ void load_v(VFrag<D>& f, uint32_t stage, int i, int g, int t) {
+  using C = Ring<D>;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int z = 0; z < D / 64; ++z) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row[i][u] != kNoRow)
-          v = __ldg(reinterpret_cast<const uint4*>(base + (size_t)row[i][u] * D + z * 64 + t * 16));
-        f.x[i][u][z] = v;
-      }
-}
-template <int D>
-__device__ __forceinline__ void load_v(VFrag<D>& f, const uint8_t* base, const uint32_t (&row)[2][4], int g) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool on = row[i][u] != kNoRow;
-      const uint8_t* a = base + (size_t)row[i][u] * D + g * (D / 8);
-      if (D == 128) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (on) v = __ldg(reinterpret_cast<const uint4*>(a));
-        f.x[i][u][0] = v.x;
-        f.x[i][u][1] = v.y;
-        f.x[i][u][D / 32 - 2] = v.z;
-        f.x[i][u][D / 32 - 1] = v.w;
-      } else {
-        uint2 v = make_uint2(0u, 0u);
-        if (on) v = __ldg(reinterpret_cast<const uint2*>(a));
-        f.x[i][u][0] = v.x;
-        f.x[i][u][1] = v.y;
-      }
+  for (int u = 0; u < 4; ++u) {
+    const int row = 16 * i + 2 * t + (u & 1) + 8 * (u >> 1);
+    if (D == 128) {
+      const uint4 v = lds128(stage + C::kRows * D + C::at(row, g));
+      f.x[u][0] = v.x;
+      f.x[u][1] = v.y;
+      f.x[u][D / 32 - 2] = v.z;
+      f.x[u][D / 32 - 1] = v.w;
+    } else {
+      const uint2 v = lds64(stage + C::kRows * D + C::at(row, g >> 1) + (g & 1) * 8);
+      f.x[u][0] = v.x;
+      f.x[u][1] = v.y;
     }
+  }
 }
 
 // Running state of one row tile in one warp. Lane (g, t) holds, for row tile part nt, rows 2 t and
@@ -206,30 +238,25 @@ struct RowState {
   float m[NT][2], mo[NT][2], l[NT][2];  // l: this lane's keys only
   uint32_t q[NT][D / 16][2];
   float qs[NT][2];   // 2^-(row exponent) * scale * log2 e
-  int pos[NT][2];
-  bool live[NT][2];
+  int pos[NT][2];    // -1: a row that does not exist
 };
 
 // ------------------------------------------------------------------ 32 keys
-// ks, ve [i][u]: key scale and log2 of the value scale of key 16 i + 8 u + g. MASK: kpos (position, or
-// -1 for none) and anchor (kept whatever the distance) of the same keys decide row by row.
-template <int D, int NT, bool MASK>
-__device__ __forceinline__ void step32(const PagedAttnParams& p, RowState<D, NT>& r, const KFrag<D>& kf,
-                                       const VFrag<D>& vf, const float (&ks)[2][2], const float (&ve)[2][2],
-                                       const int (&kpos)[2][2], const bool (&anchor)[2][2]) {
-  // ---- S^T = K Q^T
-  float s[NT][2][4];
+// S^T = K Q^T of 32 keys: s[nt][i][c], c = 2 u + e: key 16 i + 8 u + g, row 2 t + e.
+template <int D, int NT>
+__device__ __forceinline__ void scores32(const RowState<D, NT>& r, uint32_t stage, int g, int t, float (&s)[NT][2][4]) {
+  using C = Ring<D>;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 4; ++c) s[nt][i][c] = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
     for (int z = 0; z < D / 64; ++z) {
-      const uint4 x = kf.x[i][0][z], y = kf.x[i][1][z];
+      // elements (D / 4) t + 16 z .. of keys 16 i + g and 16 i + g + 8
+      const uint4 x = lds128(stage + C::at(16 * i + g, (D / 64) * t + z));
+      const uint4 y = lds128(stage + C::at(16 * i + 8 + g, (D / 64) * t + z));
       const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -240,119 +267,112 @@ __device__ __forceinline__ void step32(const PagedAttnParams& p, RowState<D, NT>
           mma16816(s[nt][i], a0, a1, a2, a3, r.q[nt][z * 4 + w][0], r.q[nt][z * 4 + w][1]);
       }
     }
-  uint32_t pb[NT][2][2];
-  uint32_t keep = 0;  // MASK: bit nt * 8 + i * 4 + c
+  }
+}
+
+// The online softmax of 32 scaled scores: new maxima, rescaled sums and accumulators, and the weights
+// as the product's column fragments. ve[i][u]: log2 of the value scale of key 16 i + 8 u + g.
+template <int D, int NT>
+__device__ __forceinline__ void weights32(RowState<D, NT>& r, float (&s)[NT][2][4], const float (&ve)[2][2],
+                                          uint32_t (&pb)[NT][2][2]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float mx[2] = {-INFINITY, -INFINITY}, mt[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int u = c >> 1, e = c & 1;
-        float x = s[nt][i][c] * (ks[i][u] * r.qs[nt][e]);
-        if (MASK) {
-          const int dist = r.pos[nt][e] - kpos[i][u];
-          const bool on = r.live[nt][e] && kpos[i][u] >= 0 && dist >= 0 && (dist < p.n || anchor[i][u]);
-          if (!on) x = -INFINITY;
-          keep |= (on ? 1u : 0u) << (nt * 8 + i * 4 + c);
-        }
-        s[nt][i][c] = x;
-        mx[e] = fmaxf(mx[e], x);
-        mt[e] = fmaxf(mt[e], x + ve[i][u]);
-      }
+    float m_ref[2], mo_ref[2], f[2];
+    bool grown = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      float mx = fmaxf(fmax3(s[nt][0][e], s[nt][0][2 + e], s[nt][1][e]), s[nt][1][2 + e]);
+      float mt = fmaxf(fmax3(s[nt][0][e] + ve[0][0], s[nt][0][2 + e] + ve[0][1], s[nt][1][e] + ve[1][0]),
+                       s[nt][1][2 + e] + ve[1][1]);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-        mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
       }
-      const float m_new = fmaxf(r.m[nt][e], mx[e]), mo_new = fmaxf(r.mo[nt][e], mt[e]);
-      const float m_ref = m_new == -INFINITY ? 0.f : m_new, mo_ref = mo_new == -INFINITY ? 0.f : mo_new;
-      r.l[nt][e] *= ex2(r.m[nt][e] - m_ref);
-      const float f = ex2(r.mo[nt][e] - mo_ref);
+      const float m_new = fmaxf(r.m[nt][e], mx), mo_new = fmaxf(r.mo[nt][e], mt);
+      m_ref[e] = m_new == -INFINITY ? 0.f : m_new;
+      mo_ref[e] = mo_new == -INFINITY ? 0.f : mo_new;
+      grown |= m_new > r.m[nt][e] || mo_new > r.mo[nt][e];
+      r.l[nt][e] *= ex2(r.m[nt][e] - m_ref[e]);
+      f[e] = ex2(r.mo[nt][e] - mo_ref[e]);
       r.m[nt][e] = m_new;
       r.mo[nt][e] = mo_new;
+    }
+    if (__any_sync(0xffffffffu, grown)) {  // otherwise every factor is 1, or its accumulator 0
 #pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        r.acc[nt][d][e] *= f;
-        r.acc[nt][d][2 + e] *= f;
-      }
+      for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float x = s[nt][i][2 * u + e];
-          r.l[nt][e] += ex2(x - m_ref);
-          s[nt][i][2 * u + e] = ex2(x + ve[i][u] - mo_ref);
-        }
+        for (int c = 0; c < 4; ++c) r.acc[nt][d][c] *= f[c & 1];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float x = s[nt][i][c];
+        r.l[nt][c & 1] += ex2(x - m_ref[c & 1]);
+        s[nt][i][c] = ex2(x + ve[i][c >> 1] - mo_ref[c & 1]);
+      }
       pb[nt][i][0] = transpose8x8(pack_half2(s[nt][i][0], s[nt][i][1]));
       pb[nt][i][1] = transpose8x8(pack_half2(s[nt][i][2], s[nt][i][3]));
     }
   }
-  // ---- a NaN among the values of a key that only some rows keep must not reach the others (0 * NaN):
-  // those bytes are taken as 0, and the rows that keep them get their NaN from a product of indicators
-  uint32_t bad = 0;
-  if (MASK) {
+}
+
+// O^T += V^T P^T of 16 keys
+template <int D, int NT>
+__device__ __forceinline__ void accumulate16(RowState<D, NT>& r, const VFrag<D>& vf, const uint32_t (&pb)[NT][2][2], int i) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int w = 0; w < D / 32; ++w) {
+    const uint32_t lo01 = __byte_perm(vf.x[0][w], vf.x[1][w], 0x5140), hi01 = __byte_perm(vf.x[0][w], vf.x[1][w], 0x7362);
+    const uint32_t lo23 = __byte_perm(vf.x[2][w], vf.x[3][w], 0x5140), hi23 = __byte_perm(vf.x[2][w], vf.x[3][w], 0x7362);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) bad |= nan_bytes(vf.x[i][u][w]);
-    bad = __any_sync(0xffffffffu, bad != 0);
+    for (int nt = 0; nt < NT; ++nt) {
+      mma16816(r.acc[nt][2 * w], cvt_e4m3x2(lo01), cvt_e4m3x2_hi(lo01), cvt_e4m3x2(lo23), cvt_e4m3x2_hi(lo23),
+               pb[nt][i][0], pb[nt][i][1]);
+      mma16816(r.acc[nt][2 * w + 1], cvt_e4m3x2(hi01), cvt_e4m3x2_hi(hi01), cvt_e4m3x2(hi23), cvt_e4m3x2_hi(hi23),
+               pb[nt][i][0], pb[nt][i][1]);
+    }
   }
-  // ---- O^T += V^T P^T
+}
+
+// A NaN among the values of a key that only some rows keep must not reach the others (0 * NaN): those
+// numbers are taken as 0, and the rows that keep the key get their NaN from a product of indicators
+// (keep: bit nt * 8 + i * 4 + c). Called only where a row masks a key; returns at once without a NaN.
+template <int D, int NT>
+__device__ __forceinline__ void confine_nan(RowState<D, NT>& r, VFrag<D>& vf, uint32_t keep, int i) {
+  uint32_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) bad |= nan_bytes(vf.x[u][w]);
+  if (!__any_sync(0xffffffffu, bad != 0)) return;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const uint32_t kb = keep >> (nt * 8 + i * 4);
+    const uint32_t b0 = transpose8x8((kb & 1 ? 0x3c00u : 0u) | (kb & 2 ? 0x3c000000u : 0u));
+    const uint32_t b1 = transpose8x8((kb & 4 ? 0x3c00u : 0u) | (kb & 8 ? 0x3c000000u : 0u));
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-      uint32_t v0 = vf.x[i][0][w], v1 = vf.x[i][1][w], v2 = vf.x[i][2][w], v3 = vf.x[i][3][w];
-      if (MASK && bad) {
-        v0 &= ~((nan_bytes(v0) >> 7) * 0xffu);
-        v1 &= ~((nan_bytes(v1) >> 7) * 0xffu);
-        v2 &= ~((nan_bytes(v2) >> 7) * 0xffu);
-        v3 &= ~((nan_bytes(v3) >> 7) * 0xffu);
-      }
-      const uint32_t lo01 = __byte_perm(v0, v1, 0x5140), hi01 = __byte_perm(v0, v1, 0x7362);
-      const uint32_t lo23 = __byte_perm(v2, v3, 0x5140), hi23 = __byte_perm(v2, v3, 0x7362);
+      float hit[2][4] = {};
+      // e4m3 1.0 (0x38) where the number is NaN; fp16 1.0 where the row keeps the key
+      uint32_t x[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma16816(r.acc[nt][2 * w], cvt_e4m3x2(lo01), cvt_e4m3x2_hi(lo01), cvt_e4m3x2(lo23),
-                 cvt_e4m3x2_hi(lo23), pb[nt][i][0], pb[nt][i][1]);
-        mma16816(r.acc[nt][2 * w + 1], cvt_e4m3x2(hi01), cvt_e4m3x2_hi(hi01), cvt_e4m3x2(hi23),
-                 cvt_e4m3x2_hi(hi23), pb[nt][i][0], pb[nt][i][1]);
-      }
-    }
-  if (MASK && bad) {
-    for (int nt = 0; nt < NT; ++nt) {
-      for (int w = 0; w < D / 32; ++w) {
-        float hit[2][4] = {};
-        for (int i = 0; i < 2; ++i) {
-          // e4m3 1.0 (0x38) where the byte is NaN; fp16 1.0 where the row keeps the key
-          uint32_t x[4];
-          for (int u = 0; u < 4; ++u) x[u] = (nan_bytes(vf.x[i][u][w]) >> 7) * 0x38u;
-          const uint32_t lo01 = __byte_perm(x[0], x[1], 0x5140), hi01 = __byte_perm(x[0], x[1], 0x7362);
-          const uint32_t lo23 = __byte_perm(x[2], x[3], 0x5140), hi23 = __byte_perm(x[2], x[3], 0x7362);
-          const uint32_t kb = keep >> (nt * 8 + i * 4);
-          const uint32_t b0 = transpose8x8((kb & 1 ? 0x3c00u : 0u) | (kb & 2 ? 0x3c000000u : 0u));
-          const uint32_t b1 = transpose8x8((kb & 4 ? 0x3c00u : 0u) | (kb & 8 ? 0x3c000000u : 0u));
-          mma16816(hit[0], cvt_e4m3x2(lo01), cvt_e4m3x2_hi(lo01), cvt_e4m3x2(lo23), cvt_e4m3x2_hi(lo23), b0, b1);
-          mma16816(hit[1], cvt_e4m3x2(hi01), cvt_e4m3x2_hi(hi01), cvt_e4m3x2(hi23), cvt_e4m3x2_hi(hi23), b0, b1);
-        }
+      for (int u = 0; u < 4; ++u) x[u] = (nan_bytes(vf.x[u][w]) >> 7) * 0x38u;
+      const uint32_t lo01 = __byte_perm(x[0], x[1], 0x5140), hi01 = __byte_perm(x[0], x[1], 0x7362);
+      const uint32_t lo23 = __byte_perm(x[2], x[3], 0x5140), hi23 = __byte_perm(x[2], x[3], 0x7362);
+      mma16816(hit[0], cvt_e4m3x2(lo01), cvt_e4m3x2_hi(lo01), cvt_e4m3x2(lo23), cvt_e4m3x2_hi(lo23), b0, b1);
+      mma16816(hit[1], cvt_e4m3x2(hi01), cvt_e4m3x2_hi(hi01), cvt_e4m3x2(hi23), cvt_e4m3x2_hi(hi23), b0, b1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-          for (int z = 0; z < D / 16; ++z)  // acc[nt][2 w + half], without a runtime register index
-            if ((z >> 1) == w && hit[z & 1][c] > 0.f) r.acc[nt][z][c] = __uint_as_float(0x7fffffffu);
-        }
+      for (int c = 0; c < 4; ++c) {
+        if (hit[0][c] > 0.f) r.acc[nt][2 * w][c] = __uint_as_float(0x7fffffffu);
+        if (hit[1][c] > 0.f) r.acc[nt][2 * w + 1][c] = __uint_as_float(0x7fffffffu);
       }
     }
   }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) vf.x[u][w] &= ~((nan_bytes(vf.x[u][w]) >> 7) * 0xffu);
 }
 
 // ------------------------------------------------------------------ rows of a row tile
@@ -374,7 +394,7 @@ __device__ __forceinline__ void begin_rows(const PagedAttnParams& p, RowState<D,
       for (int z = 0; z < D / 64; ++z)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off + z * 64 + t * 16 + y * 8);
+          const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off + t * (D / 4) + z * 16 + y * 8);
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -409,8 +429,7 @@ __device__ __forceinline__ void begin_rows(const PagedAttnParams& p, RowState<D,
     for (int e = 0; e < 2; ++e) {
       const int re = rt * R + nt * 8 + 2 * t + e;
       r.qs[nt][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
-      r.live[nt][e] = re < rows;
-      r.pos[nt][e] = q.lead + re / p.G;
+      r.pos[nt][e] = re < rows ? q.lead + re / p.G : -1;
       r.m[nt][e] = r.mo[nt][e] = -INFINITY;
       r.l[nt][e] = 0.f;
     }
@@ -482,22 +501,20 @@ __device__ __forceinline__ void end_rows(const PagedAttnParams& p, RowState<D, N
 struct PageRun {
   int first;
   uint32_t row;  // first row of the page for this head (id * Hkv + h) * P, kNoRow: none
-  float ks, ve;
+  uint32_t ex;   // exponents of its two scales
 };
 __device__ __forceinline__ PageRun load_pages(const PagedAttnParams& p, int seq, int h, int first, int len, int lane) {
   PageRun r;
   r.first = first;
   r.row = kNoRow;
-  r.ks = 0.f;
-  r.ve = 0.f;
+  r.ex = 0;
   const int pg = first + lane;
   if (pg < p.max_pages && ((long long)pg << p.log_page) < len) {
     const int id = __ldg(p.table + (long long)seq * p.max_pages + pg);
     if (id >= 0 && id < p.num_pages) {
       const size_t sc = (size_t)id * p.Hkv + h;
       r.row = (uint32_t)(sc << p.log_page);
-      r.ks = __ldg(p.k_scale + sc);
-      r.ve = log2_of_scale(__ldg(p.v_scale + sc));
+      r.ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
     } else {
       record_failure(p.err, nullptr, SEP_ERR_INDEX);
     }
@@ -505,118 +522,143 @@ __device__ __forceinline__ PageRun load_pages(const PagedAttnParams& p, int seq,
   return r;
 }
 
-// Rows of 32 consecutive keys from c0 (a multiple of 32) for this lane's fragments.
-__device__ __forceinline__ void dense_rows(const PagedAttnParams& p, const PageRun& pr, int c0, int end, int g, int t,
-                                           uint32_t (&kr)[2][2], uint32_t (&vr)[2][4],
-                                           float (&ks)[2][2], float (&ve)[2][2]) {
+// 32 consecutive keys from c0 (a multiple of 32): their two 16-key halves lie in one page each.
+struct Run32 {
+  uint32_t row[2];  // pool row of each half's first key
+  uint32_t ex[2];   // exponents of its page's scales
+  int left[2];      // keys of the half that exist
+};
+__device__ __forceinline__ Run32 run32(const PagedAttnParams& p, const PageRun& pr, int c0, int end) {
+  Run32 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int x = c0 + 16 * i;
     const int src = ((x >> p.log_page) - pr.first) & 31;
     const uint32_t base = __shfl_sync(0xffffffffu, pr.row, src);
-    const float s = __shfl_sync(0xffffffffu, pr.ks, src), e = __shfl_sync(0xffffffffu, pr.ve, src);
-    const uint32_t row = base + (uint32_t)(x & ((1 << p.log_page) - 1));
-    const int left = base == kNoRow ? 0 : min(16, end - x);  // rows of this tile that exist
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      kr[i][u] = 8 * u + g < left ? row + 8 * u + g : kNoRow;
-      ks[i][u] = s;
-      ve[i][u] = e;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int y = 2 * t + (u & 1) + 8 * (u >> 1);
-      vr[i][u] = y < left ? row + y : kNoRow;
-    }
+    r.ex[i] = __shfl_sync(0xffffffffu, pr.ex, src);
+    r.row[i] = base + (uint32_t)(x & ((1 << p.log_page) - 1));
+    r.left[i] = base == kNoRow ? 0 : max(0, min(16, end - x));
   }
+  return r;
+}
+template <int D>
+__device__ __forceinline__ void fetch_run(const PagedAttnParams& p, uint32_t stage, const Run32& x, int lane) {
+  fetch32<D>(p, stage, lane, [&](int r, bool* on) {
+    const int i = r >> 4;
+    *on = (r & 15) < x.left[i];
+    return x.row[i] + (r & 15);
+  });
 }
 
-// Keys [c0, c1) of the window part (c0 a multiple of 64).
+// Keys [c0, c1) of the window part (c0 a multiple of 64), for queries at positions lo .. hi. Two stages
+// of 32 keys: one is computed on while the other arrives.
 template <int D, int NT>
 __device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int len,
-                                            int lo, int hi, int c0, int c1, int lane) {
+                                            int lo, int hi, int c0, int c1, uint32_t ring, int lane) {
+  using C = Ring<D>;
   const int g = lane >> 2, t = lane & 3;
   const int run = 32 << p.log_page;
   PageRun pr = load_pages(p, seq, h, c0 >> p.log_page, len, lane);
-  KFrag<D> kf;
-  VFrag<D> vf;
-  uint32_t kr[2][2], vr[2][4];
-  float ks[2][2], ve[2][2], ksn[2][2], ven[2][2];
-  dense_rows(p, pr, c0, c1, g, t, kr, vr, ks, ve);
-  load_k(kf, p.k_pages, kr, t);
-  load_v(vf, p.v_pages, vr, g);
+  Run32 x = run32(p, pr, c0, c1), xn = run32(p, pr, min(c0 + 32, c1 - 1 & ~31), c1);
+  fetch_run<D>(p, ring, x, lane);
+  if (c0 + 32 < c1) fetch_run<D>(p, ring + C::kBytes, xn, lane);
+  else copy_commit();
+  uint32_t stage = ring;
+#pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
-    const bool more = c + 32 < c1;
-    int kpos[2][2];
-    bool anchor[2][2];
+    copy_wait<1>();
+    __syncwarp();
+    float s[NT][2][4];
+    scores32(r, stage, g, t, s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float ks = key_scale(x.ex[i]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][i][e] *= ks * r.qs[nt][e & 1];
+    }
     // every row keeps all 32 keys: none behind the earliest query, none outside the last one's window
-    const bool full = c + 32 <= c1 && c + 31 <= lo && hi - c < p.n &&
-                      __all_sync(0xffffffffu, kr[0][0] != kNoRow && kr[1][0] != kNoRow);
+    const bool full = c + 31 <= lo && hi - c < p.n && x.left[0] == 16 && x.left[1] == 16;
+    uint32_t keep = 0;
     if (!full) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int j = c + 16 * i + 8 * u + g;
-          kpos[i][u] = kr[i][u] != kNoRow ? j : -1;
-          anchor[i][u] = false;
-          if (kr[i][u] != kNoRow && hi - c >= p.n) {
-            const int id = (int)((kr[i][u] >> p.log_page) / (uint32_t)p.Hkv);
-            anchor[i][u] = j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + (j & ((1 << p.log_page) - 1))) != 0;
+          const int y = 8 * u + g, j = c + 16 * i + y;
+          const bool there = y < x.left[i];
+          bool anchor = false;
+          if (there && hi - c >= p.n) {
+            const int id = (int)((x.row[i] >> p.log_page) / (uint32_t)p.Hkv);
+            anchor = j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + (j & ((1 << p.log_page) - 1))) != 0;
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int dist = r.pos[nt][e] - j;  // rows that do not exist have position -1
+              const bool on = there && dist >= 0 && (dist < p.n || anchor);
+              if (!on) s[nt][i][2 * u + e] = -INFINITY;
+              keep |= (on ? 1u : 0u) << (nt * 8 + i * 4 + 2 * u + e);
+            }
         }
-      step32<D, NT, true>(p, r, kf, vf, ks, ve, kpos, anchor);
+    }
+    const float v0 = value_log2(x.ex[0]), v1 = value_log2(x.ex[1]);
+    const float ve[2][2] = {{v0, v0}, {v1, v1}};
+    uint32_t pb[NT][2][2];
+    weights32(r, s, ve, pb);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      VFrag<D> vf;
+      load_v(vf, stage, i, g, t);
+      if (!full) confine_nan(r, vf, keep, i);
+      accumulate16(r, vf, pb, i);
+    }
+    x = xn;
+    __syncwarp();  // every lane is done with the stage
+    if (c + 64 < c1) {
+      if (c + 64 - (pr.first << p.log_page) >= run) pr = load_pages(p, seq, h, (c + 64) >> p.log_page, len, lane);
+      xn = run32(p, pr, c + 64, c1);
+      fetch_run<D>(p, stage, xn, lane);
     } else {
-      step32<D, NT, false>(p, r, kf, vf, ks, ve, kpos, anchor);
+      copy_commit();
     }
-    if (more) {
-      if (c + 32 - (pr.first << p.log_page) >= run) pr = load_pages(p, seq, h, (c + 32) >> p.log_page, len, lane);
-      dense_rows(p, pr, c + 32, c1, g, t, kr, vr, ksn, ven);
-      load_k(kf, p.k_pages, kr, t);
-      load_v(vf, p.v_pages, vr, g);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          ks[i][u] = ksn[i][u];
-          ve[i][u] = ven[i][u];
-        }
-    }
+    stage = stage == ring ? ring + C::kBytes : ring;
   }
+  copy_wait<0>();
 }
 
 // ------------------------------------------------------------------ tiles left of the window
 // Positions [c0, c1) (at most kScan, c0 a multiple of kScan): the keys with j < a or a separator flag,
 // kept by every row, are listed in shared memory and read 32 at a time.
 struct Listed {
-  uint32_t row;
-  float ks, ve;
+  uint32_t row, ex;  // pool row, exponents of its page's scales
 };
 template <int D, int NT>
 __device__ __forceinline__ void scan_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int c0, int c1,
-                                          Listed* list, int lane) {
+                                          Listed* list, uint32_t ring, int lane) {
+  using C = Ring<D>;
   const int g = lane >> 2, t = lane & 3;
-  // 16 positions per lane: always inside one page
-  const int j0 = c0 + 16 * lane;
-  uint32_t bits = 0, row = 0;
-  float ks = 0.f, ve = 0.f;
+  // kScan / 32 positions per lane: always inside one page
+  constexpr int kPer = kScan / 32;
+  const int j0 = c0 + kPer * lane;
+  uint32_t bits = 0, row = 0, ex = 0;
   if (j0 < c1) {
     const int pg = j0 >> p.log_page;
     const int id = pg < p.max_pages ? __ldg(p.table + (long long)seq * p.max_pages + pg) : -1;
     if (id >= 0 && id < p.num_pages) {
-      const int off = (int)(j0 & ((1 << p.log_page) - 1));
-      const uint4 f = __ldg(reinterpret_cast<const uint4*>(p.flags + ((size_t)id << p.log_page) + off));
-      const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+      const int off = j0 & ((1 << p.log_page) - 1);
+      const uint2 f = __ldg(reinterpret_cast<const uint2*>(p.flags + ((size_t)id << p.log_page) + off));
 #pragma unroll
-      for (int x = 0; x < 16; ++x) bits |= ((w[x >> 2] >> (8 * (x & 3))) & 0xffu ? 1u : 0u) << x;
+      for (int x = 0; x < kPer; ++x) bits |= (((x < 4 ? f.x : f.y) >> (8 * (x & 3))) & 0xffu ? 1u : 0u) << x;
       const int init = p.a - j0;  // initial tokens
-      if (init > 0) bits |= init >= 16 ? 0xffffu : (1u << init) - 1u;
+      if (init > 0) bits |= init >= kPer ? (1u << kPer) - 1u : (1u << init) - 1u;
       const int left = c1 - j0;
-      if (left < 16) bits &= (1u << left) - 1u;
+      if (left < kPer) bits &= (1u << left) - 1u;
       const size_t sc = (size_t)id * p.Hkv + h;
       row = (uint32_t)(sc << p.log_page) + off;
-      ks = __ldg(p.k_scale + sc);
-      ve = log2_of_scale(__ldg(p.v_scale + sc));
+      ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
     } else {
       record_failure(p.err, nullptr, SEP_ERR_INDEX);
     }
@@ -634,49 +676,67 @@ __device__ __forceinline__ void scan_keys(const PagedAttnParams& p, RowState<D, 
   while (bits) {
     const int x = __ffs(bits) - 1;
     bits &= bits - 1;
-    list[at++] = Listed{row + x, ks, ve};
+    list[at++] = Listed{row + x, ex};
   }
   __syncwarp();
-  KFrag<D> kf;
-  VFrag<D> vf;
-  uint32_t kr[2][2], vr[2][4];
+  if (total == 0) return;
+  auto fetch = [&](uint32_t stage, int b) {
+    fetch32<D>(p, stage, lane, [&](int r, bool* on) {
+      *on = b + r < total;
+      return list[min(b + r, total - 1)].row;
+    });
+  };
+  fetch(ring, 0);
+  if (32 < total) fetch(ring + C::kBytes, 32);
+  else copy_commit();
+  uint32_t stage = ring;
+#pragma unroll 1
   for (int b = 0; b < total; b += 32) {
-    float kss[2][2], vee[2][2];
-    int kpos[2][2];
-    bool anchor[2][2];
+    copy_wait<1>();
+    __syncwarp();
+    float s[NT][2][4], ve[2][2];
+    scores32(r, stage, g, t, s);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int x = b + 16 * i + 8 * u + g;
-        const Listed e = list[min(x, total - 1)];
-        kr[i][u] = x < total ? e.row : kNoRow;
-        kss[i][u] = e.ks;
-        vee[i][u] = e.ve;
-        kpos[i][u] = x < total ? 0 : -1;  // position 0: behind no row with a position
-        anchor[i][u] = true;
-      }
+        const uint32_t e = list[min(x, total - 1)].ex;
+        ve[i][u] = value_log2(e);
+        const float ks = key_scale(e);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int x = b + 16 * i + 2 * t + (u & 1) + 8 * (u >> 1);
-        vr[i][u] = x < total ? list[x].row : kNoRow;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            s[nt][i][2 * u + z] = x < total ? s[nt][i][2 * u + z] * (ks * r.qs[nt][z]) : -INFINITY;
       }
+    uint32_t pb[NT][2][2];
+    weights32(r, s, ve, pb);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      VFrag<D> vf;
+      load_v(vf, stage, i, g, t);
+      accumulate16(r, vf, pb, i);
     }
-    load_k(kf, p.k_pages, kr, t);
-    load_v(vf, p.v_pages, vr, g);
-    if (b + 32 <= total) step32<D, NT, false>(p, r, kf, vf, kss, vee, kpos, anchor);
-    else step32<D, NT, true>(p, r, kf, vf, kss, vee, kpos, anchor);
+    __syncwarp();
+    if (b + 64 < total) fetch(stage, b + 64);
+    else copy_commit();
+    stage = stage == ring ? ring + C::kBytes : ring;
   }
+  copy_wait<0>();
 }
 
 // ------------------------------------------------------------------ kernel
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int R = 8 * NT;
-  extern __shared__ long long s_base[];  // [S + 1], then the scan lists of the warps
+  extern __shared__ __align__(16) uint8_t s_raw[];  // rings of the warps, scan lists, tile numbers
   __shared__ long long s_part[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Listed* list = reinterpret_cast<Listed*>(s_base + p.S + 1) + warp * kScan;
+  const uint32_t ring = smem_u32(s_raw) + warp * (Ring<D>::kStages * Ring<D>::kBytes);
+  Listed* list = reinterpret_cast<Listed*>(s_raw + kWarps * Ring<D>::kStages * Ring<D>::kBytes) + warp * kScan;
+  long long* s_base = reinterpret_cast<long long*>(s_raw + kWarps * (Ring<D>::kStages * Ring<D>::kBytes +
+                                                                     kScan * (int)sizeof(Listed)));  // [S + 1]
   grid_dep_wait();
   grid_dep_launch_next();
 
@@ -750,13 +810,13 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const __grid_co
     const RowTile w = row_tile(p, q, rt, R);
     begin_rows<D, NT>(p, r, q, h, rt, g, t);
     for (int y = ta; y < min(tb, w.ns); ++y)
-      scan_keys<D, NT>(p, r, seq, h, y * kScan, min(w.w0, (y + 1) * kScan), list, lane);
+      scan_keys<D, NT>(p, r, seq, h, y * kScan, min(w.w0, (y + 1) * kScan), list, ring, lane);
     const int da = max(ta, w.ns) - w.ns, db = min(tb - w.ns, w.nd);
     if (da < db) {
       const int lo = q.lead + rt * R / p.G;
       const int hi = q.lead + min(q.nq - 1, (rt * R + R - 1) / p.G);
       window_keys<D, NT>(p, r, seq, h, q.len, lo, hi, w.w0 + da * kDense,
-                         min(w.kend, w.w0 + db * kDense), lane);
+                         min(w.kend, w.w0 + db * kDense), ring, lane);
     }
     const bool whole = ta == 0 && tb == per_rt;
     // a warp's run has at most one row tile that began before it (slot 0) and one that ends after it
@@ -769,63 +829,97 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const __grid_co
 // ------------------------------------------------------------------ join of the parts
 // One CTA per (query token, query head). Its row tile's tiles belong to warps w0 .. w1; with w0 = w1
 // the row is written already. Part of warp w0 is in its slot 1 unless its run begins with this row
-// tile; the others begin with it (slot 0).
+// tile; the others begin with it (slot 0). The factors of all parts come first, in shared memory; the
+// accumulators are then added in the order of the warps, kJoinGroups interleaved sums.
+constexpr int kJoinThreads = 256;
 template <int D, int NT>
-__global__ void __launch_bounds__(128) seppaged_join_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int R = 8 * NT, LPR = D / 4, GR = 128 / LPR;  // lanes per row, groups of lanes
+__global__ void __launch_bounds__(kJoinThreads) seppaged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int R = 8 * NT, LPR = D / 4, GR = kJoinThreads / LPR;  // lanes per row, groups of lanes
   __shared__ float4 s_acc[GR][LPR];
-  __shared__ float s_st[GR][3];
+  __shared__ float s_f[kMaxWarps];
+  __shared__ float s_red[3][kJoinThreads / 32];
   grid_dep_wait();
   grid_dep_launch_next();
   const int tok = blockIdx.x / p.Hq, hq = blockIdx.x - tok * p.Hq;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // sequence of the token: last s with indptr[s] <= tok
-  int lo = 0, hi = p.S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.indptr + mid) <= tok) lo = mid;
-    else hi = mid;
+  int seq = -1;
+  for (int s0 = 0; s0 < p.S; s0 += kJoinThreads) {
+    const int hit = __syncthreads_count(s0 + tid < p.S && __ldg(p.indptr + s0 + tid) <= tok);
+    seq += hit;
+    if (hit < min(kJoinThreads, p.S - s0)) break;
   }
-  const SeqInfo q = seq_info(p, lo);
+  if (seq < 0) return;
+  const SeqInfo q = seq_info(p, seq);
   if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
   const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
   const int rt = row / R, lr = row - rt * R;
   const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
-  const long long t0 = p.base[lo] + ((long long)h * nrt + rt) * per_rt, t1 = t0 + per_rt;
+  const long long t0 = p.base[seq] + ((long long)h * nrt + rt) * per_rt, t1 = t0 + per_rt;
   const long long per = (p.base[p.S] + p.nwarps - 1) / p.nwarps;
-  const int w0 = (int)(t0 / per), w1 = (int)((t1 - 1) / per);
-  if (w0 == w1) return;
-  const int grp = tid / LPR, c = tid - grp * LPR;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float mo = -INFINITY, m = -INFINITY, l = 0.f;
-  auto add = [&](float4 a, float mo2, float m2, float l2) {
-    const float mo_n = fmaxf(mo, mo2), m_n = fmaxf(m, m2);
-    const float mor = mo_n == -INFINITY ? 0.f : mo_n, mr = m_n == -INFINITY ? 0.f : m_n;
-    const float f0 = ex2(mo - mor), f1 = ex2(mo2 - mor);
-    l = l * ex2(m - mr) + l2 * ex2(m2 - mr);
-    acc.x = acc.x * f0 + a.x * f1;
-    acc.y = acc.y * f0 + a.y * f1;
-    acc.z = acc.z * f0 + a.z * f1;
-    acc.w = acc.w * f0 + a.w * f1;
-    mo = mo_n;
-    m = m_n;
-  };
-#pragma unroll 4
-  for (int w = w0 + grp; w <= w1; w += GR) {
-    const float* part = part_of<D, R>(p, w, w == w0 && t0 > (long long)w0 * per ? 1 : 0);
-    const float4 st = *reinterpret_cast<const float4*>(part + (size_t)R * D + lr * 4);
-    const float4 a = *reinterpret_cast<const float4*>(part + (size_t)lr * D + c * 4);
-    add(a, st.x, st.y, st.z);
+  const int w0 = (int)(t0 / per), w1 = (int)((t1 - 1) / per), parts = w1 - w0 + 1;
+  if (parts == 1) return;
+  const int first_slot = t0 > (long long)w0 * per ? 1 : 0;
+  auto part = [&](int i) -> const float* { return part_of<D, R>(p, w0 + i, i == 0 ? first_slot : 0); };
+  // ---- maxima
+  float mo = -INFINITY, m = -INFINITY;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const float4 st = *reinterpret_cast<const float4*>(part(i) + (size_t)R * D + lr * 4);
+    mo = fmaxf(mo, st.x);
+    m = fmaxf(m, st.y);
   }
-  s_acc[grp][c] = acc;
-  if (c == 0) {
-    s_st[grp][0] = mo;
-    s_st[grp][1] = m;
-    s_st[grp][2] = l;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  if (lane == 0) {
+    s_red[0][warp] = mo;
+    s_red[1][warp] = m;
   }
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    mo = fmaxf(mo, s_red[0][w]);
+    m = fmaxf(m, s_red[1][w]);
+  }
+  const float mor = mo == -INFINITY ? 0.f : mo, mr = m == -INFINITY ? 0.f : m;
+  // ---- factors of the parts and the row sum
+  float l = 0.f;
+  for (int i = tid; i < parts; i += kJoinThreads) {
+    const float4 st = *reinterpret_cast<const float4*>(part(i) + (size_t)R * D + lr * 4);
+    s_f[i] = ex2(st.x - mor);
+    l += st.z * ex2(st.y - mr);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_red[2][warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[2][w];
+  // ---- accumulators
+  const int grp = tid / LPR, c = tid - grp * LPR;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = grp; i < parts; i += GR) {
+    const float4 a = *reinterpret_cast<const float4*>(part(i) + (size_t)lr * D + c * 4);
+    const float f = s_f[i];
+    acc.x = fmaf(a.x, f, acc.x);
+    acc.y = fmaf(a.y, f, acc.y);
+    acc.z = fmaf(a.z, f, acc.z);
+    acc.w = fmaf(a.w, f, acc.w);
+  }
+  s_acc[grp][c] = acc;
+  __syncthreads();
   if (grp != 0) return;
-  for (int x = 1; x < GR; ++x) add(s_acc[x][c], s_st[x][0], s_st[x][1], s_st[x][2]);
+#pragma unroll
+  for (int x = 1; x < GR; ++x) {
+    acc.x += s_acc[x][c].x;
+    acc.y += s_acc[x][c].y;
+    acc.z += s_acc[x][c].z;
+    acc.w += s_acc[x][c].w;
+  }
   const bool none = m == -INFINITY && !(l != l);
   float2 f = join_factors(mo, m, l);
   if (none || mo == -INFINITY) f = make_float2(0.f, none ? 0.f : 1.f / l);
@@ -837,13 +931,14 @@ __global__ void __launch_bounds__(128) seppaged_join_kernel(const __grid_constan
 
 template <int D, int NT>
 cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
-  const size_t smem = (size_t)(p.S + 1) * sizeof(long long) + (size_t)kWarps * kScan * sizeof(Listed);
+  const size_t smem = (size_t)(p.S + 1) * sizeof(long long) +
+                      (size_t)kWarps * (kScan * sizeof(Listed) + Ring<D>::kStages * Ring<D>::kBytes);
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !set[dev].load()) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev].store(true);
   }
@@ -854,7 +949,7 @@ cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
   p.nwarps = grid * kWarps;
   e = launch_chained(paged_attn_kernel<D, NT>, dim3(grid), dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(seppaged_join_kernel<D, NT>, dim3((unsigned)p.T * p.Hq), dim3(128), 0, stream, p);
+  return launch_chained(seppaged_join_kernel<D, NT>, dim3((unsigned)p.T * p.Hq), dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace

@@ -12,6 +12,7 @@ import ctypes
 import dataclasses
 import math
 import os
+import struct
 
 import torch
 
@@ -82,23 +83,6 @@ class _SepCacheState(ctypes.Structure):
                 ("k_slots", ctypes.c_void_p), ("v_slots", ctypes.c_void_p),
                 ("slot_pos", ctypes.c_void_p), ("slot_sep", ctypes.c_void_p),
                 ("meta", ctypes.c_void_p), ("rope_freq", ctypes.c_void_p)]
-
-
-class _SepRope(ctypes.Structure):
-    _fields_ = [("freq", ctypes.c_void_p), ("d_rot", ctypes.c_int32),
-                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
-
-
-class _SepRopeTensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
-                ("y_stride", ctypes.c_int64 * 3), ("H", ctypes.c_int32)]
-
-
-class _SepPagedState(ctypes.Structure):
-    _fields_ = [("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
-                ("page", ctypes.c_int32), ("k_pages", ctypes.c_void_p),
-                ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("flags", ctypes.c_void_p), ("rope", _SepRope)]
 
 
 def _check(status: int, what: str):
@@ -431,6 +415,30 @@ class SepCache:
 # ------------------------------------------------------------------ rotary positions
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 INT32_MAX = 2 ** 31 - 1
+# The structs of the C ABI as packed bytes: the library reads them during the call only, and packing
+# costs the caller a fraction of what building ctypes structures does (decode steps are bound by the
+# host side of these calls).
+_ROPE = struct.Struct("@Piif4x")            # SepRope
+_ROPE_TENSOR = struct.Struct("@PP6qi4x")    # SepRopeTensor
+_PAGED = struct.Struct("@4i5PPiif4x")       # SepPagedState
+
+
+def _raw_stream(device_index):
+    """The current stream of a device as an integer handle."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def _one_device(first, *rest):
+    """_same_device for the calls of a decode step: indices first, names only to report."""
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise SepError(f"a tensor of the call is on {t.device}, the others on {first.device}")
+    if dev != _current_device_index():
+        raise SepError(f"the call's tensors are on {first.device} but the current CUDA device is "
+                       f"cuda:{_current_device_index()}; make {first.device} current "
+                       "(torch.cuda.device) for this call")
+    return dev
 
 
 def _strided(t, dtypes, name, shape):
@@ -456,8 +464,9 @@ class SepRope:
     interleaved: bool
     magnitude: float
 
-    def _c(self):
-        return _SepRope(self.freq.data_ptr(), self.d_rot, int(self.interleaved), self.magnitude)
+    def _packed(self):
+        """The C struct SepRope."""
+        return _ROPE.pack(self.freq.data_ptr(), self.d_rot, self.interleaved, self.magnitude)
 
 
 def _scaled_frequencies(d_rot, theta, scaling):
@@ -548,63 +557,86 @@ def sep_rope_table(d_rot, theta, interleaved=False, scaling=None, device="cuda")
                    bool(interleaved), magnitude)
 
 
+def _rope_side(name, t, lead, nd, dtype, y):
+    """Checks one tensor of a rotary call and its output; returns (output, packed argument)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != nd:
+        raise SepError(f"{name} must be a {nd}-D tensor")
+    shape, st = t.shape, t.stride()
+    if tuple(shape[:-2]) != tuple(lead):
+        raise SepError(f"{name} has shape {tuple(shape)}, expected {tuple(lead)} + (heads, d)")
+    if t.dtype is not dtype:
+        raise SepError(f"{name} has dtype {t.dtype}, q has {dtype}")
+    if st[-1] != 1 and shape[-1] > 1:
+        raise SepError(f"{name}: the last dimension must be contiguous")
+    if not t.is_cuda:
+        raise SepError(f"{name} must be on a CUDA device (there is no CPU path)")
+    ptr = t.data_ptr()
+    if y is None:
+        y = torch.empty_like(t, memory_format=torch.contiguous_format)
+        ys = y.stride()
+        yptr = y.data_ptr()
+    else:
+        _strided(y, (dtype,), f"out {name}", shape)
+        ys = y.stride()
+        yptr = y.data_ptr()
+        if any(n > 1 and x == 0 for n, x in zip(shape, ys)):
+            raise SepError(f"out {name} is an expanded view: its rows share memory")
+        if yptr != ptr and _overlap(t, y):
+            raise SepError(f"out {name} overlaps {name} without being it")
+        if yptr == ptr and ys != st and t.numel() > 0:
+            raise SepError(f"out {name} starts where {name} does with other strides")
+    if nd == 3:
+        return y, _ROPE_TENSOR.pack(ptr, yptr, 0, st[0], st[1], 0, ys[0], ys[1], shape[-2])
+    return y, _ROPE_TENSOR.pack(ptr, yptr, st[0], st[1], st[2], ys[0], ys[1], ys[2], shape[-2])
+
+
 def _rope_call(fn, what, q, k, positions, rope, out):
     if not isinstance(rope, SepRope):
         raise SepError("rope must come from sep_rope_table")
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise SepError("q must be a [tokens, heads, d] or [B, L, heads, d] tensor")
-    lead, d = tuple(q.shape[:-2]), q.shape[-1]
+    nd, shape, dtype = q.dim(), q.shape, q.dtype
+    lead, d = shape[:-2], shape[-1]
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise SepError(f"q has dtype {dtype}, expected one of {tuple(_DTYPES)}")
     if rope.d_rot > d:
         raise SepError(f"d_rot = {rope.d_rot} is larger than the head dimension {d}")
-    tensors = [("q", q)] if k is None else [("q", q), ("k", k)]
-    for name, t in tensors:
-        heads = t.shape[-2] if isinstance(t, torch.Tensor) and t.dim() == q.dim() else 0
-        _strided(t, tuple(_DTYPES), name, lead + (heads, d))
-        if t.dtype != q.dtype:
-            raise SepError(f"{name} has dtype {t.dtype}, q has {q.dtype}")
+    if k is not None and isinstance(k, torch.Tensor) and k.shape[-1] != d:
+        raise SepError(f"k has head dimension {k.shape[-1]}, q has {d}")
     if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
         raise SepError("positions must be an int32 or int64 tensor")
-    if tuple(positions.shape) not in (lead, lead[-1:]):
-        raise SepError(f"positions has shape {tuple(positions.shape)}, expected {lead} "
-                       f"or {lead[-1:]}")
+    if positions.shape != lead and positions.shape != lead[-1:]:
+        raise SepError(f"positions has shape {tuple(positions.shape)}, expected {tuple(lead)} "
+                       f"or {tuple(lead[-1:])}")
     if not positions.is_contiguous():
         raise SepError("positions must be contiguous")
+    yq = yk = None
+    if out is not None:
+        out = out if isinstance(out, (tuple, list)) else (out,)
+        if len(out) not in (1, 2) or (len(out) == 2 and out[1] is not None) != (k is not None):
+            raise SepError("out must hold one tensor for each of q and k")
+        yq, yk = out[0], out[1] if k is not None else None
+        if yq is None:
+            raise SepError("out must hold one tensor for each of q and k")
+    yq, qa = _rope_side("q", q, lead, nd, dtype, yq)
+    ka = None
+    if k is not None:
+        yk, ka = _rope_side("k", k, lead, nd, dtype, yk)
     if not positions.is_cuda:
         raise SepError("positions must be on a CUDA device (there is no CPU path)")
-    if out is None:
-        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for _, t in tensors)
-    out = tuple(x for x in (out if isinstance(out, (tuple, list)) else (out,)) if x is not None)
-    if len(out) != len(tensors):
-        raise SepError(f"out must hold {len(tensors)} tensor(s)")
-    for (name, t), y in zip(tensors, out):
-        _strided(y, (q.dtype,), f"out {name}", t.shape)
-        if any(n > 1 and x == 0 for n, x in zip(y.shape, y.stride())):
-            raise SepError(f"out {name} is an expanded view: its rows share memory")
-        if y.data_ptr() != t.data_ptr() and _overlap(t, y):
-            raise SepError(f"out {name} overlaps {name} without being it")
-        if y.data_ptr() == t.data_ptr() and y.stride() != t.stride() and t.numel() > 0:
-            raise SepError(f"out {name} starts where {name} does with other strides")
-    _same_device(q.device, *tensors, *((f"out {n}", y) for (n, _), y in zip(tensors, out)),
-                 ("positions", positions), ("rope", rope.freq))
-    result = out if k is not None else (out[0], None)
-    if q.numel() == 0 and (k is None or k.numel() == 0):
-        return result
-    if any(t.numel() == 0 for _, t in tensors):
+    dev = _one_device(q, k, yq, yk, positions, rope.freq)
+    if q.numel() == 0 or (k is not None and k.numel() == 0):
+        if q.numel() == 0 and (k is None or k.numel() == 0):
+            return yq, yk
         raise SepError("q and k need at least one head each")
-    B, L = (1, lead[0]) if len(lead) == 1 else lead
+    B, L = (1, lead[0]) if nd == 3 else lead
     if B * L > INT32_MAX:
         raise SepError("more than 2^31 - 1 tokens")
-    args = []
-    for (_, t), y in zip(tensors, out):
-        xs, ys = ((0,) + s if len(lead) == 1 else s for s in (t.stride()[:-1], y.stride()[:-1]))
-        args.append(_SepRopeTensor(t.data_ptr(), y.data_ptr(), (ctypes.c_int64 * 3)(*xs),
-                                   (ctypes.c_int64 * 3)(*ys), t.shape[-2]))
-    rc = rope._c()
-    _check(fn(ctypes.byref(rc), _DTYPES[q.dtype], B, L, d, _ptr(positions),
-              int(positions.dtype == torch.int64), L if positions.dim() == 2 else 0,
-              ctypes.byref(args[0]), ctypes.byref(args[1]) if len(args) > 1 else None, _stream()),
-           what)
-    return result
+    _check(fn(rope._packed(), code, B, L, d, positions.data_ptr(),
+              1 if positions.dtype is torch.int64 else 0,
+              L if nd == 4 and positions.dim() == 2 else 0, qa, ka, _raw_stream(dev)), what)
+    return yq, yk
 
 
 def _extent(t):
@@ -702,61 +734,74 @@ class SepPagedCache:
                                f"expected {tuple(dst.shape)}")
             dst.copy_(sd[k])
 
-    def _c(self):
-        rope = _SepRope(None, 0, 0, 1.0) if self.rope is None else self.rope._c()
-        return _SepPagedState(self.num_pages, self.Hkv, self.d, self.page,
-                              self.k_pages.data_ptr(), self.v_pages.data_ptr(),
-                              self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                              self.flags.data_ptr(), rope)
+    def _packed(self):
+        """The C struct SepPagedState."""
+        r = self.rope
+        return _PAGED.pack(self.num_pages, self.Hkv, self.d, self.page, self.k_pages.data_ptr(),
+                           self.v_pages.data_ptr(), self.k_scale.data_ptr(),
+                           self.v_scale.data_ptr(), self.flags.data_ptr(),
+                           *((0, 0, 0, 1.0) if r is None else
+                             (r.freq.data_ptr(), r.d_rot, r.interleaved, r.magnitude)))
 
-    def _plan(self, page_table, seq_lens, indptr):
-        """Checks the index tensors and the state; returns (S, max_pages)."""
-        S, max_pages = _dims(page_table, 2, "page_table")
-        _cuda(page_table, torch.int32, "page_table")
-        _cuda(seq_lens, torch.int32, "seq_lens", (S,))
-        _cuda(indptr, torch.int32, "indptr", (S + 1,))
-        if S < 1 or max_pages < 1:
-            raise SepError("page_table needs at least one sequence and one page")
-        _cuda(self.k_pages, torch.float8_e4m3fn, "k_pages",
-              (self.num_pages, self.Hkv, self.page, self.d))
-        _cuda(self.v_pages, torch.float8_e4m3fn, "v_pages", tuple(self.k_pages.shape))
-        _cuda(self.k_scale, torch.float32, "k_scale", (self.num_pages, self.Hkv))
-        _cuda(self.v_scale, torch.float32, "v_scale", (self.num_pages, self.Hkv))
-        _cuda(self.flags, torch.uint8, "flags", (self.num_pages, self.page))
-        return S, max_pages
-
-    def _on_device(self, *named):
-        _same_device(self.k_pages.device, *((k, getattr(self, k)) for k in self._STATE),
-                     ("rope", self.rope.freq if self.rope is not None else None), *named)
+    def _state(self):
+        """Checks the cache's own tensors (a caller may put its own buffers in their place)."""
+        pages, per_head = (self.num_pages, self.Hkv, self.page, self.d), (self.num_pages, self.Hkv)
+        for name, t, dtype, shape in (("k_pages", self.k_pages, torch.float8_e4m3fn, pages),
+                                      ("v_pages", self.v_pages, torch.float8_e4m3fn, pages),
+                                      ("k_scale", self.k_scale, torch.float32, per_head),
+                                      ("v_scale", self.v_scale, torch.float32, per_head),
+                                      ("flags", self.flags, torch.uint8, pages[::2])):
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+                _cuda(t, dtype, name, shape)
 
     @staticmethod
-    def _rows(t, name):
-        """Token and head strides of a [T, H, d] tensor read 16 bytes at a time."""
-        if t.data_ptr() % 16 != 0 or t.stride(0) % 8 != 0 or t.stride(1) % 8 != 0:
+    def _plan(page_table, seq_lens, indptr):
+        """Checks the index tensors; returns (S, max_pages)."""
+        S, max_pages = _dims(page_table, 2, "page_table")
+        if S < 1 or max_pages < 1:
+            raise SepError("page_table needs at least one sequence and one page")
+        for name, t, shape in (("page_table", page_table, (S, max_pages)),
+                               ("seq_lens", seq_lens, (S,)), ("indptr", indptr, (S + 1,))):
+            if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not torch.int32
+                    or not t.is_contiguous() or not t.is_cuda):
+                _cuda(t, torch.int32, name, shape)
+        return S, max_pages
+
+    @staticmethod
+    def _rows(t, name, T, H, d):
+        """Address and token and head strides of a [T, H, d] tensor that is read 16 bytes at a
+        time."""
+        if not isinstance(t, torch.Tensor) or t.shape != (T, H, d) or not t.is_cuda or \
+                (t.dtype is not torch.bfloat16 and t.dtype is not torch.float16):
+            _strided(t, (torch.bfloat16, torch.float16), name, (T, H, d))
+        st, ptr = t.stride(), t.data_ptr()
+        if st[2] != 1:
+            raise SepError(f"{name}: the last dimension must be contiguous")
+        if ptr % 16 != 0 or st[0] % 8 != 0 or st[1] % 8 != 0:
             raise SepError(f"{name}: the start and the strides of tokens and heads must be "
                            "multiples of 16 bytes")
-        return t.stride(0), t.stride(1)
+        return ptr, st[0], st[1]
 
     def seppaged_append(self, k, v, page_table, seq_lens, indptr, sep=None):
         """Stores the newest tokens' k, v [T, Hkv, d] (bf16 or fp16, k without rotary embedding
         when the cache has a rope) and separator flags sep [T] uint8 (None: no separators)."""
         T = _dims(k, 3, "k")[0]
-        for name, t in (("k", k), ("v", v)):
-            _strided(t, (torch.bfloat16, torch.float16), name, (T, self.Hkv, self.d))
-        if k.dtype != v.dtype:
+        rows = (self._rows(k, "k", T, self.Hkv, self.d), self._rows(v, "v", T, self.Hkv, self.d))
+        if k.dtype is not v.dtype:
             raise SepError(f"v has dtype {v.dtype}, k has {k.dtype}")
         S, max_pages = self._plan(page_table, seq_lens, indptr)
+        self._state()
         if sep is not None:
             _cuda(sep, torch.uint8, "sep", (T,))
-        self._on_device(("k", k), ("v", v), ("page_table", page_table), ("seq_lens", seq_lens),
-                        ("indptr", indptr), ("sep", sep))
+        dev = _one_device(k, v, page_table, seq_lens, indptr, sep, self.k_pages, self.v_pages,
+                          self.k_scale, self.v_scale, self.flags,
+                          self.rope.freq if self.rope is not None else None)
         if T == 0:
             return
-        st = self._c()
-        _check(_lib.seppaged_append(ctypes.byref(st), _DTYPES[k.dtype], _ptr(k),
-                                    *self._rows(k, "k"), _ptr(v), *self._rows(v, "v"), _ptr(sep),
-                                    T, S, max_pages, _ptr(page_table), _ptr(seq_lens),
-                                    _ptr(indptr), _stream()), "seppaged_append")
+        _check(_lib.seppaged_append(self._packed(), _DTYPES[k.dtype], *rows[0], *rows[1],
+                                    sep.data_ptr() if sep is not None else None, T, S, max_pages,
+                                    page_table.data_ptr(), seq_lens.data_ptr(), indptr.data_ptr(),
+                                    _raw_stream(dev)), "seppaged_append")
 
     def seppaged_attn(self, q, page_table, seq_lens, indptr, a=0, n=None, scale=None, out=None,
                       lse=None, workspace=None):
@@ -765,10 +810,11 @@ class SepPagedCache:
         keeps every key up to p. Rows that keep nothing: O = 0, LSE = -inf; rows outside
         indptr's range are left as they are in `out` and `lse`."""
         T, Hq, d = _dims(q, 3, "q")
-        _strided(q, (torch.bfloat16, torch.float16), "q", (T, Hq, self.d))
         if Hq < 1 or Hq % self.Hkv != 0:
             raise SepError(f"Hq = {Hq} is not a multiple of Hkv = {self.Hkv}")
+        row = self._rows(q, "q", T, Hq, self.d)
         S, max_pages = self._plan(page_table, seq_lens, indptr)
+        self._state()
         if S > 4096:
             raise SepError(f"{S} sequences: at most 4096")
         if T * Hq > INT32_MAX:
@@ -777,22 +823,24 @@ class SepPagedCache:
         if not 0 <= a <= INT32_MAX or not 0 <= n <= INT32_MAX:
             raise SepError(f"a = {a} and n = {n} must be between 0 and 2^31 - 1")
         scale = self.d ** -0.5 if scale is None else scale
-        o = torch.empty(T, Hq, d, dtype=q.dtype, device=q.device) if out is None else out
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
-        _cuda(o, q.dtype, "out", (T, Hq, d))
-        _cuda(lse, torch.float32, "lse", (T, Hq))
-        nbytes = seppaged_attn_workspace_size(S, self.d)
-        ws = _workspace(nbytes, q.device, workspace)
-        self._on_device(("q", q), ("page_table", page_table), ("seq_lens", seq_lens),
-                        ("indptr", indptr), ("out", o), ("lse", lse), ("workspace", ws))
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            _cuda(out, q.dtype, "out", (T, Hq, d))
+        if lse is None:
+            lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+        else:
+            _cuda(lse, torch.float32, "lse", (T, Hq))
+        dev = _one_device(q, page_table, seq_lens, indptr, out, lse, workspace, self.k_pages,
+                          self.v_pages, self.k_scale, self.v_scale, self.flags)
+        ws = _workspace(seppaged_attn_workspace_size(S, self.d), q.device, workspace)
         if T == 0:
-            return o, lse
-        st = self._c()
-        _check(_lib.seppaged_attn(ctypes.byref(st), _DTYPES[q.dtype], _ptr(q),
-                                  *self._rows(q, "q"), Hq, T, S, max_pages, _ptr(page_table),
-                                  _ptr(seq_lens), _ptr(indptr), int(a), n, float(scale), _ptr(o),
-                                  _ptr(lse), _ptr(ws), ws.numel(), _stream()), "seppaged_attn")
-        return o, lse
+            return out, lse
+        _check(_lib.seppaged_attn(self._packed(), _DTYPES[q.dtype], *row, Hq, T, S, max_pages,
+                                  page_table.data_ptr(), seq_lens.data_ptr(), indptr.data_ptr(),
+                                  int(a), n, float(scale), out.data_ptr(), lse.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), _raw_stream(dev)), "seppaged_attn")
+        return out, lse
 
 
 def seppaged_attn_workspace_size(S, d) -> int:

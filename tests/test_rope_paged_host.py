@@ -199,15 +199,42 @@ def test_attn_binding_refusals(monkeypatch):
 
 
 # ------------------------------------------------------------------ C entry points
-class _State(ctypes.Structure):
-    _fields_ = S._SepPagedState._fields_
+class _SepRope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("d_rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class _SepRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
+                ("y_stride", ctypes.c_int64 * 3), ("H", ctypes.c_int32)]
+
+
+class _SepPagedState(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("flags", ctypes.c_void_p), ("rope", _SepRope)]
+
+
+def test_packed_structs_have_the_c_layout():
+    assert S._ROPE.size == ctypes.sizeof(_SepRope)
+    assert S._ROPE_TENSOR.size == ctypes.sizeof(_SepRopeTensor)
+    assert S._PAGED.size == ctypes.sizeof(_SepPagedState)
+    r = _SepRope.from_buffer_copy(S._ROPE.pack(5, 6, True, 1.5))
+    assert (r.freq, r.d_rot, r.interleaved, r.magnitude) == (5, 6, 1, 1.5)
+    t = _SepRopeTensor.from_buffer_copy(S._ROPE_TENSOR.pack(*range(1, 10)))
+    assert (t.x, t.y, list(t.x_stride), list(t.y_stride), t.H) == (1, 2, [3, 4, 5], [6, 7, 8], 9)
+    p = _SepPagedState.from_buffer_copy(S._PAGED.pack(*range(1, 10), 10, 11, 0, 2.0))
+    assert (p.num_pages, p.Hkv, p.d, p.page, p.k_pages, p.v_pages, p.k_scale, p.v_scale, p.flags) == \
+        tuple(range(1, 10))
+    assert (p.rope.freq, p.rope.d_rot, p.rope.interleaved, p.rope.magnitude) == (10, 11, 0, 2.0)
 
 
 def _state(**kw):
     base = dict(num_pages=4, Hkv=2, d=64, page=16, k_pages=P16, v_pages=P16, k_scale=P16, v_scale=P16,
-                flags=P16, rope=S._SepRope(None, 0, 0, 1.0))
+                flags=P16, rope=_SepRope(None, 0, 0, 1.0))
     base.update(kw)
-    return S._SepPagedState(**base)
+    return _SepPagedState(**base)
 
 
 def _append(st=None, dtype=0, k=P16, ktok=128, khead=64, T=3, S_=2, mp=2, table=P16, lens=P16, ip=P16):
@@ -226,9 +253,9 @@ def test_append_entry_refusals():
     assert _append(dtype=2) == UNSUPPORTED and _append(dtype=7) == UNSUPPORTED
     assert _append(k=P16 + 8) == MISALIGNED and _append(ktok=132) == MISALIGNED
     assert _append(st=_state(v_pages=P16 + 8)) == MISALIGNED
-    assert _append(st=_state(rope=S._SepRope(P16, 66, 0, 1.0))) == INVALID
-    assert _append(st=_state(rope=S._SepRope(P16, 7, 0, 1.0))) == INVALID
-    assert _append(st=_state(rope=S._SepRope(None, 64, 0, 1.0))) == INVALID
+    assert _append(st=_state(rope=_SepRope(P16, 66, 0, 1.0))) == INVALID
+    assert _append(st=_state(rope=_SepRope(P16, 7, 0, 1.0))) == INVALID
+    assert _append(st=_state(rope=_SepRope(None, 64, 0, 1.0))) == INVALID
 
 
 def _attn(st=None, dtype=0, q=P16, Hq=4, T=3, S_=2, a=0, n=8, o=P16, ws=P16, nbytes=1 << 40):
@@ -251,8 +278,8 @@ def test_attn_entry_refusals():
 def test_rope_entry_refusals():
     def call(fn=S._lib.sep_rope_fwd, rope=(P16, 64, 0, 1.0), dtype=0, B=1, L=4, d=64, pos=P16, pos64=0, x=P16,
              H=2):
-        r = S._SepRope(*rope)
-        t = S._SepRopeTensor(x, P16, (ctypes.c_int64 * 3)(0, 128, 64), (ctypes.c_int64 * 3)(0, 128, 64), H)
+        r = _SepRope(*rope)
+        t = _SepRopeTensor(x, P16, (ctypes.c_int64 * 3)(0, 128, 64), (ctypes.c_int64 * 3)(0, 128, 64), H)
         return fn(ctypes.byref(r), dtype, B, L, d, pos, pos64, 0, ctypes.byref(t), None, None)
 
     for fn in (S._lib.sep_rope_fwd, S._lib.sep_rope_bwd):
