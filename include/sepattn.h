@@ -328,7 +328,7 @@ int sep_attn_fwd_noalloc(const sep_bf16* q, const sep_bf16* k, const sep_bf16* v
  * from d_rot on are then not touched); other overlaps are not allowed. k may be NULL. Any
  * element-aligned address works; 16-byte aligned rows and halves take 16-byte accesses.
  * pos: int32 (pos64 = 0) or int64 [L] per batch, batch b's at pos + b * pos_stride (0: shared).
- * dtype BF16, F16 or F32. 2 <= d_rot <= d <= 512, d_rot even; B * L <= 2^31 - 1.
+ * dtype BF16, F16 or F32. 2 <= d_rot <= d <= 512, d_rot even, H <= 8192; B * L <= 2^31 - 1.
  */
 typedef struct SepRope {
   const double* freq;  /* [d_rot / 2] angle per position step of each pair (device) */

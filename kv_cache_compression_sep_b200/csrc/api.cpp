@@ -320,7 +320,8 @@ static int rope_impl(const SepRope* rope, int dtype, int B, int L, int d, const 
   if (reinterpret_cast<uintptr_t>(pos) % (pos64 ? 8 : 4) != 0) return SEP_ERR_MISALIGNED;
   for (const SepRopeTensor* t : {q, k}) {
     if (!t) continue;
-    if (!t->x || !t->y || t->H < 1 || t->H > 65536) return SEP_ERR_INVALID_ARG;
+    if (!t->x || !t->y || t->H < 1) return SEP_ERR_INVALID_ARG;
+    if (t->H > 8192) return SEP_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(t->x) % es != 0 || reinterpret_cast<uintptr_t>(t->y) % es != 0)
       return SEP_ERR_MISALIGNED;
   }

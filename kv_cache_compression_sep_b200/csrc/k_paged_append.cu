@@ -10,15 +10,19 @@
 // that it holds already are re-expressed when it does. Values that are not finite are stored as
 // NaN (e4m3 has no infinity), so that they show in the attention instead of passing as numbers.
 //
-// Work: one team of P * d / 32 threads per (page touched, KV head), 32 elements of K and of V per
-// thread, kept in fp32 registers from the load over the maximum to the store: one read of the
-// 16-bit rows, one write of the bytes; HBM bounds it. The (cos, sin) table of the page's new rows
-// is formed once per CTA and used by all its heads.
+// Two kernels. Pages that receive many rows (prompts): a CTA per (page, group of heads) holds a head's
+// rows in registers from the load over the maximum to the store, so each is read and written once;
+// HBM bounds it, and instruction issue next (half the issue slots at 128 registers and 16 warps per SM; 24
+// warps spill: 125 us against 73 us for 8 prompts of 8192 tokens, 8 heads of 128: 313 MB, 4.3 TB/s).
+// The (cos, sin) table of the page's rows is formed once per CTA, the next head's rows are requested
+// before the current one's maximum is known, a team's maximum is one shared-memory atomic per warp. Few rows (decode): a warp per
+// (page, head), bound by the chain of dependent loads (offsets, length, page number, old scale).
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "sep_common.cuh"
 #include "sep_launch.h"
@@ -56,19 +60,12 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;  // false for NaN too
-}
+constexpr float kFltMax = 3.402823466e38f;
 
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
   const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-// x / s; infinities become NaN (the conversion would saturate them)
-__device__ __forceinline__ float scaled(float x, float inv) {
-  return fabsf(x) <= 3.402823466e38f ? x * inv : __uint_as_float(0x7fc00000u);
 }
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w, int hi) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(hi ? w >> 16 : w & 0xffffu),
@@ -81,25 +78,25 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float ratio) {
   return to_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
-constexpr int kChunks = 4;  // 8-element chunks of K and of V per thread
-
+// Eight 16-bit values, kept packed until they are used, as four fp32 pairs.
 template <typename T>
-struct __align__(16) Vec8 {
-  T v[8];
+__device__ __forceinline__ void widen8(const uint4& a, float2* x) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int z = 0; z < 4; ++z)
+    x[z] = std::is_same<T, __nv_bfloat16>::value
+               ? make_float2(__uint_as_float(w[z] << 16), __uint_as_float(w[z] & 0xffff0000u))
+               : __half22float2(*reinterpret_cast<const __half2*>(&w[z]));
+}
+
+// The work of one call that a unit stands for: new rows r0 .. r0 + nrow - 1 (positions) of page id.
+struct Unit {
+  int id, slot0, nrow;
+  long long r0, tok0;  // position and token of the first row
 };
-
-template <typename T, int D>
-__global__ void __launch_bounds__(512) paged_append_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ float2 s_cs[];  // [P][d_rot / 2]
-  __shared__ float s_max[2][16];    // per warp: K, V
-  const SepPagedState& st = p.st;
-  const int P = 1 << p.log_page, nthr = blockDim.x, tid = threadIdx.x;
-  constexpr int CPR = D / 8;  // chunks per row
-  grid_dep_wait();
-  grid_dep_launch_next();
-
-  // ---- the sequence and page of this unit
-  const long long unit = blockIdx.x;
+// Finds unit `unit`; false: nothing to do (the same answer in every thread of the CTA).
+__device__ __forceinline__ bool find_unit(const AppendParams& p, long long unit, Unit* u) {
+  const int nthr = blockDim.x, tid = threadIdx.x;
   int seq = -1;
   for (int s0 = 0; s0 < p.S; s0 += nthr) {
     const int s = s0 + tid;
@@ -107,178 +104,401 @@ __global__ void __launch_bounds__(512) paged_append_kernel(const __grid_constant
     seq += hit;
     if (hit < min(nthr, p.S - s0)) break;
   }
-  if (seq < 0) return;
+  if (seq < 0) return false;
   const int i0 = __ldg(p.indptr + seq), i1 = __ldg(p.indptr + seq + 1);
   const long long len = __ldg(p.lens + seq);
   const long long lead = len - ((long long)i1 - i0);  // position of token i0; negative: padding
   const long long first = max(lead, 0ll);
   const long long pg = (first >> p.log_page) + (unit - unit_start(p, seq, i0));
   const long long r0 = max(first, pg << p.log_page), r1 = min(len, (pg + 1) << p.log_page);
-  if (r0 >= r1) return;
-  const long long tok0 = i0 + (r0 - lead);  // token of row r0
-  int id = -1;
-  if (pg < p.max_pages) id = __ldg(p.table + (long long)seq * p.max_pages + pg);
-  if (id < 0 || id >= st.num_pages || tok0 < 0 || tok0 + (r1 - r0) > p.T) {
+  if (r0 >= r1) return false;
+  u->r0 = r0;
+  u->tok0 = i0 + (r0 - lead);
+  u->nrow = (int)(r1 - r0);
+  u->slot0 = (int)(r0 & ((1 << p.log_page) - 1));
+  u->id = pg < p.max_pages ? __ldg(p.table + (long long)seq * p.max_pages + pg) : -1;
+  if (u->id < 0 || u->id >= p.st.num_pages || u->tok0 < 0 || u->tok0 + u->nrow > p.T) {
     if (tid == 0) record_failure(p.err, nullptr, SEP_ERR_INDEX);
-    return;
+    return false;
   }
-  const int slot0 = (int)(r0 & (P - 1)), nrow = (int)(r1 - r0);
+  return true;
+}
 
-  const int h = st.rope.d_rot >> 1;
-  for (int e = tid; e < nrow * h; e += nthr) {
-    float c, s;
-    rope_angle(r0 + e / h, __ldg(st.rope.freq + e % h), &c, &s);
-    s_cs[e] = make_float2(c * st.rope.magnitude, s * st.rope.magnitude);
-  }
-  if (blockIdx.y == 0)
-    for (int r = tid; r < nrow; r += nthr)
-      st.flags[(size_t)id * P + slot0 + r] = p.sep ? p.sep[tok0 + r] : 0;
-  __syncthreads();
-
-  const int team_size = P * CPR / kChunks, teams = nthr / team_size;
-  const int team = tid / team_size, tt = tid - team * team_size;
-  const int h_end = min(st.Hkv, (int)(blockIdx.y + 1) * p.heads_per_cta);
-  for (int hb = blockIdx.y * p.heads_per_cta; hb < h_end; hb += teams) {
-    const int head = hb + team;
-    const bool on = head < h_end;
-    float kx[kChunks][8], vx[kChunks][8];
-    float km = 0.f, vm = 0.f;
-    const T* kb = static_cast<const T*>(p.k) + tok0 * p.k_tok + (long long)head * p.k_head;
-    const T* vb = static_cast<const T*>(p.v) + tok0 * p.v_tok + (long long)head * p.v_head;
+// A key row is taken in D / 16 items of two 8-element groups at e0 and e1: a group and its partners in
+// the half layout where halves are whole groups, else 16 neighbours.
+struct Item {
+  int e0, e1;
+};
+template <bool PAIRED>
+__device__ __forceinline__ Item item_of(const SepRope& r, int j) {
+  const int h = r.d_rot >> 1;
+  if (PAIRED && 8 * j < h) return Item{8 * j, 8 * j + h};
+  return Item{16 * j, 16 * j + 8};  // PAIRED: 8 j >= h is 16 j >= d_rot, past the rotated part
+}
+// The item's 16 elements in fp32, turned. cs: (cos, sin) of the row's pairs; row: its first element
+// (read again where partners lie in other groups).
+template <typename T, bool PAIRED>
+__device__ __forceinline__ void turn(const SepRope& r, Item it, const uint4& a, const uint4& b, const T* row,
+                                     const float2* cs, float2 (&x)[8]) {
+  widen8<T>(a, x);
+  widen8<T>(b, x + 4);
+  if (it.e0 >= r.d_rot) return;
+  if (PAIRED) {
+    // e0 and the row's pairs are multiples of 8; two pairs of the table per load
+    const float4* c4 = reinterpret_cast<const float4*>(cs + it.e0);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int ch = tt + c * team_size, row = ch / CPR - slot0, e0 = (ch % CPR) * 8;
-      const bool live = on && row >= 0 && row < nrow;
-      Vec8<T> a = {}, b = {};
-      if (live) {
-        a = *reinterpret_cast<const Vec8<T>*>(kb + row * p.k_tok + e0);
-        b = *reinterpret_cast<const Vec8<T>*>(vb + row * p.v_tok + e0);
+    for (int z = 0; z < 4; ++z) {
+      const float4 c = c4[z];
+      const float2 x1 = x[z], x2 = x[4 + z];
+      x[z] = make_float2(__fmaf_rn(x1.x, c.x, -__fmul_rn(x2.x, c.y)), __fmaf_rn(x1.y, c.z, -__fmul_rn(x2.y, c.w)));
+      x[4 + z] = make_float2(__fmaf_rn(x2.x, c.x, __fmul_rn(x1.x, c.y)), __fmaf_rn(x2.y, c.z, __fmul_rn(x1.y, c.w)));
+    }
+  } else if (r.interleaved) {
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if (it.e0 + 2 * z < r.d_rot) {
+        const float2 c = cs[(it.e0 >> 1) + z];
+        x[z] = make_float2(__fmaf_rn(x[z].x, c.x, -__fmul_rn(x[z].y, c.y)),
+                           __fmaf_rn(x[z].y, c.x, __fmul_rn(x[z].x, c.y)));
       }
+  } else {
+    const int h = r.d_rot >> 1;
 #pragma unroll
-      for (int z = 0; z < 8; ++z) {
-        kx[c][z] = to_float(a.v[z]);
-        vx[c][z] = to_float(b.v[z]);
-      }
-      if (live && e0 < st.rope.d_rot) {
-        const float2* cs = s_cs + row * h;
-        const T* kr = kb + row * p.k_tok;
-        if (st.rope.interleaved) {
-#pragma unroll
-          for (int z = 0; z < 8; z += 2) {
-            if (e0 + z < st.rope.d_rot) {
-              const float2 w = cs[(e0 + z) >> 1];
-              const float x1 = kx[c][z], x2 = kx[c][z + 1];
-              kx[c][z] = __fmaf_rn(x1, w.x, -__fmul_rn(x2, w.y));
-              kx[c][z + 1] = __fmaf_rn(x2, w.x, __fmul_rn(x1, w.y));
-            }
-          }
-        } else if ((h & 7) == 0) {  // the partners are one 16-byte group
-          const bool upper = e0 >= h;
-          const Vec8<T> o = *reinterpret_cast<const Vec8<T>*>(kr + (upper ? e0 - h : e0 + h));
-          const float2* ce = cs + (upper ? e0 - h : e0);
-#pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            const float2 w = ce[z];
-            const float part = to_float(o.v[z]);
-            kx[c][z] = upper ? __fmaf_rn(kx[c][z], w.x, __fmul_rn(part, w.y))
-                             : __fmaf_rn(kx[c][z], w.x, -__fmul_rn(part, w.y));
-          }
-        } else {
-#pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            const int e = e0 + z;
-            if (e < st.rope.d_rot) {
-              const bool upper = e >= h;
-              const float2 w = cs[upper ? e - h : e];
-              const float part = to_float(kr[upper ? e - h : e + h]);
-              kx[c][z] = upper ? __fmaf_rn(kx[c][z], w.x, __fmul_rn(part, w.y))
-                               : __fmaf_rn(kx[c][z], w.x, -__fmul_rn(part, w.y));
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int z = 0; z < 8; ++z) {
-        km = fmaxf(km, finite_abs(kx[c][z]));
-        vm = fmaxf(vm, finite_abs(vx[c][z]));
+    for (int z = 0; z < 16; ++z) {
+      const int e = it.e0 + z;
+      if (e < r.d_rot) {
+        const bool upper = e >= h;
+        const float2 c = cs[upper ? e - h : e];
+        const float part = to_float(row[upper ? e - h : e + h]);
+        float& v = z & 1 ? x[z >> 1].y : x[z >> 1].x;
+        v = upper ? __fmaf_rn(v, c.x, __fmul_rn(part, c.y)) : __fmaf_rn(v, c.x, -__fmul_rn(part, c.y));
       }
     }
-    // ---- largest magnitudes of the team's rows
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
-      vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-    }
-    if ((tid & 31) == 0) {
-      s_max[0][tid >> 5] = km;
-      s_max[1][tid >> 5] = vm;
-    }
-    const size_t sc = (size_t)id * st.Hkv + (on ? head : 0);
-    const float old_k = slot0 > 0 && on ? st.k_scale[sc] : 0.f;
-    const float old_v = slot0 > 0 && on ? st.v_scale[sc] : 0.f;
-    __syncthreads();  // every thread has read the old scales and written its maximum
-    const int w0 = team * team_size >> 5, w1 = (team + 1) * team_size >> 5;
-    for (int w = w0; w < w1; ++w) {
-      km = fmaxf(km, s_max[0][w]);
-      vm = fmaxf(vm, s_max[1][w]);
-    }
-    const float new_k = fmaxf(old_k, km > 0.f ? pow2(scale_exponent(km)) : 0.f);
-    const float new_v = fmaxf(old_v, vm > 0.f ? pow2(scale_exponent(vm)) : 0.f);
-    if (on) {
-      if (tt == 0) {
-        st.k_scale[sc] = new_k;
-        st.v_scale[sc] = new_v;
-      }
-      // 1 / 0 for a page of zeros: 0, so that zeros stay zeros and NaN stays NaN
-      const float inv_k = new_k > 0.f ? 1.f / new_k : 0.f, inv_v = new_v > 0.f ? 1.f / new_v : 0.f;
-      const bool grow_k = old_k > 0.f && new_k > old_k, grow_v = old_v > 0.f && new_v > old_v;
-      uint8_t* kp = st.k_pages + sc * P * D;
-      uint8_t* vp = st.v_pages + sc * P * D;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int ch = tt + c * team_size, slot = ch / CPR, row = slot - slot0;
-        uint2* kd = reinterpret_cast<uint2*>(kp + (size_t)ch * 8);
-        uint2* vd = reinterpret_cast<uint2*>(vp + (size_t)ch * 8);
-        if (row >= 0 && row < nrow) {
-          const float* a = kx[c];
-          const float* b = vx[c];
-          *kd = make_uint2(to_e4m3x4(scaled(a[0], inv_k), scaled(a[1], inv_k), scaled(a[2], inv_k),
-                                     scaled(a[3], inv_k)),
-                           to_e4m3x4(scaled(a[4], inv_k), scaled(a[5], inv_k), scaled(a[6], inv_k),
-                                     scaled(a[7], inv_k)));
-          *vd = make_uint2(to_e4m3x4(scaled(b[0], inv_v), scaled(b[1], inv_v), scaled(b[2], inv_v),
-                                     scaled(b[3], inv_v)),
-                           to_e4m3x4(scaled(b[4], inv_v), scaled(b[5], inv_v), scaled(b[6], inv_v),
-                                     scaled(b[7], inv_v)));
-        } else if (slot < slot0) {
-          if (grow_k) {
-            const uint2 w = *kd;
-            const float ratio = old_k * inv_k;
-            *kd = make_uint2(rescale_e4m3x4(w.x, ratio), rescale_e4m3x4(w.y, ratio));
-          }
-          if (grow_v) {
-            const uint2 w = *vd;
-            const float ratio = old_v * inv_v;
-            *vd = make_uint2(rescale_e4m3x4(w.x, ratio), rescale_e4m3x4(w.y, ratio));
-          }
-        }
-      }
-    }
-    __syncthreads();  // s_max is reused by the next heads
   }
 }
 
-template <typename T, int D>
+// Largest finite magnitude of 16 values. A NaN is ignored by fmaxf and stays NaN in e4m3; an infinity
+// would be saturated there, so it is made a NaN here, in a second look that only its finder takes.
+__device__ __forceinline__ float confine_infinities(float2 (&x)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    if (fabsf(x[z].x) > kFltMax) x[z].x = __uint_as_float(0x7fc00000u);
+    if (fabsf(x[z].y) > kFltMax) x[z].y = __uint_as_float(0x7fc00000u);
+    top = fmaxf(top, fmaxf(fabsf(x[z].x), fabsf(x[z].y)));
+  }
+  return top;
+}
+__device__ __forceinline__ float largest(float2 (&x)[8]) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    m0 = fmaxf(m0, fabsf(x[z].x));
+    m1 = fmaxf(m1, fabsf(x[z].y));
+  }
+  const float top = fmaxf(m0, m1);
+  return top > kFltMax ? confine_infinities(x) : top;
+}
+// The largest magnitudes of the low and of the high halves of 16 packed values: magnitudes of 16-bit
+// floats are ordered as integers.
+__device__ __forceinline__ uint32_t magnitudes(const uint4& a, const uint4& b) {
+  constexpr uint32_t kMag = 0x7fff7fffu;
+  const uint32_t m0 = __vmaxu2(__vmaxu2(a.x & kMag, a.y & kMag), __vmaxu2(a.z & kMag, a.w & kMag));
+  const uint32_t m1 = __vmaxu2(__vmaxu2(b.x & kMag, b.y & kMag), __vmaxu2(b.z & kMag, b.w & kMag));
+  return __vmaxu2(m0, m1);
+}
+// The largest finite magnitude of 16 packed values; *odd: some value is not finite.
+template <typename T>
+__device__ __forceinline__ float largest_packed(const uint4& a, const uint4& b, bool* odd) {
+  constexpr uint32_t kInf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  const uint32_t m = magnitudes(a, b), top = max(m & 0xffffu, m >> 16);
+  *odd = top >= kInf;
+  if (*odd) {
+    float2 x[8];
+    widen8<T>(a, x);
+    widen8<T>(b, x + 4);
+    return confine_infinities(x);
+  }
+  const uint16_t bits = (uint16_t)top;
+  return to_float(*reinterpret_cast<const T*>(&bits));
+}
+// Eight values over the scale as e4m3.
+__device__ __forceinline__ uint2 quantised(const float2* x, float inv) {
+  return make_uint2(to_e4m3x4(x[0].x * inv, x[0].y * inv, x[1].x * inv, x[1].y * inv),
+                    to_e4m3x4(x[2].x * inv, x[2].y * inv, x[3].x * inv, x[3].y * inv));
+}
+// Sixteen packed values over the scale; odd: some are not finite.
+template <typename T>
+__device__ __forceinline__ uint4 quantised_packed(const uint4& a, const uint4& b, float inv, bool odd) {
+  float2 x[8];
+  widen8<T>(a, x);
+  widen8<T>(b, x + 4);
+  if (odd) confine_infinities(x);
+  const uint2 lo = quantised(x, inv), hi = quantised(x + 4, inv);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+// New scale of a page from the old one (0 where its rows all are new) and the new rows' maximum.
+__device__ __forceinline__ float grown(float old, float top) {
+  return fmaxf(old, top > 0.f ? pow2(scale_exponent(top)) : 0.f);
+}
+// 1 / scale; 0 for a page of zeros, so that zeros stay zeros and NaN stays NaN.
+__device__ __forceinline__ float inverse(float s) { return s > 0.f ? 1.f / s : 0.f; }
+// Rows 0 .. slot0 - 1 of a page in a larger scale, by nthr threads.
+template <int D>
+__device__ __forceinline__ void reexpress(uint8_t* page, int slot0, float ratio, int tid, int nthr) {
+  for (int e = tid; e < slot0 * (D / 16); e += nthr) {
+    uint4 w = *reinterpret_cast<uint4*>(page + (size_t)e * 16);
+    w.x = rescale_e4m3x4(w.x, ratio);
+    w.y = rescale_e4m3x4(w.y, ratio);
+    w.z = rescale_e4m3x4(w.z, ratio);
+    w.w = rescale_e4m3x4(w.w, ratio);
+    *reinterpret_cast<uint4*>(page + (size_t)e * 16) = w;
+  }
+}
+
+// ------------------------------------------------------------------ many rows per page
+// Teams of P * D / 32 threads, one head each at a time; a thread has the same item of two rows, P / 2
+// apart, of K and of V.
+template <typename T, int D, bool PAIRED>
+__global__ void __launch_bounds__(512) paged_append_page_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ __align__(16) float2 s_cs[];  // [P][d_rot / 2]
+  __shared__ uint32_t s_top[3][8][2];             // by turns: per team, K and V (bits of floats >= 0)
+  const SepPagedState& st = p.st;
+  const int P = 1 << p.log_page, nthr = blockDim.x, tid = threadIdx.x;
+  constexpr int IPR = D / 16;  // items per row
+  constexpr uint32_t kInf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  grid_dep_wait();
+  grid_dep_launch_next();
+  Unit u;
+  if (!find_unit(p, blockIdx.x, &u)) return;
+
+  const int log_team = p.log_page + (D == 128 ? 2 : 1);  // P * IPR / 2
+  const int team = tid >> log_team, tt = tid & ((1 << log_team) - 1), teams = nthr >> log_team;
+  const int h_begin = blockIdx.y * p.heads_per_cta, h_end = min(st.Hkv, h_begin + p.heads_per_cta);
+  const int j = tt % IPR, slot = tt / IPR, h = st.rope.d_rot >> 1;
+  const Item it = item_of<PAIRED>(st.rope, j);
+  bool live[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int row = slot + c * (P / 2) - u.slot0;
+    live[c] = row >= 0 && row < u.nrow;
+  }
+  // the thread's first row, at its item (not read where there is none)
+  const T* kt = static_cast<const T*>(p.k) + (u.tok0 + slot - u.slot0) * p.k_tok;
+  const T* vt = static_cast<const T*>(p.v) + (u.tok0 + slot - u.slot0) * p.v_tok + 16 * j;
+  const long long k_hop = P / 2 * p.k_tok, v_hop = P / 2 * p.v_tok;
+  uint4 ka[2], kb[2], va[2], vb[2];
+  auto load = [&](int head) {
+    const T* k = kt + head * p.k_head;
+    const T* v = vt + head * p.v_head;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (live[c] && head < h_end) {
+        ka[c] = *reinterpret_cast<const uint4*>(k + c * k_hop + it.e0);
+        kb[c] = *reinterpret_cast<const uint4*>(k + c * k_hop + it.e1);
+        va[c] = *reinterpret_cast<const uint4*>(v + c * v_hop);
+        vb[c] = *reinterpret_cast<const uint4*>(v + c * v_hop + 8);
+      }
+  };
+#pragma unroll
+  for (int c = 0; c < 2; ++c) ka[c] = kb[c] = va[c] = vb[c] = make_uint4(0u, 0u, 0u, 0u);
+  load(h_begin + team);
+  if (tt < 2) s_top[0][team][tt] = 0;
+  angle_table(s_cs, u.nrow, h, st.rope.freq, st.rope.magnitude, st.rope.magnitude, tid, nthr,
+              [&](int r) { return (double)(u.r0 + r); });
+  if (blockIdx.y == 0)
+    for (int r = tid; r < u.nrow; r += nthr)
+      st.flags[(size_t)u.id * P + u.slot0 + r] = p.sep ? p.sep[u.tok0 + r] : 0;
+  __syncthreads();
+
+  const float2* cs = s_cs + (slot - u.slot0) * h;
+  int turn_no = 0;  // its maxima are collected, the next turn's set to 0, before the turn's barrier
+#pragma unroll 1
+  for (int head = h_begin + team; head - team < h_end; head += teams) {
+    const bool on = head < h_end;
+    float2 kx[2][8];
+    uint4 wa[2], wb[2];  // this head's values
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      wa[c] = va[c];
+      wb[c] = vb[c];
+      if (live[c])
+        turn<T, PAIRED>(st.rope, it, ka[c], kb[c], kt + head * p.k_head + c * k_hop, cs + c * (P / 2) * h, kx[c]);
+    }
+    load(head + teams);
+    // ---- largest magnitudes; rows that do not exist are zeros. NaN is ignored and stays NaN in e4m3;
+    // infinities would be saturated there: their finder takes a second look and makes them NaN.
+    float km = 0.f;
+    uint32_t vmax = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (live[c]) {
+#pragma unroll
+        for (int z = 0; z < 8; ++z) km = fmaxf(km, fmaxf(fabsf(kx[c][z].x), fabsf(kx[c][z].y)));
+        vmax = __vmaxu2(vmax, magnitudes(wa[c], wb[c]));
+      }
+    vmax = max(vmax & 0xffffu, vmax >> 16);
+    const bool odd = vmax >= kInf;  // values that are not finite
+    if (km > kFltMax) {
+      km = 0.f;
+      if (live[0]) km = confine_infinities(kx[0]);
+      if (live[1]) km = fmaxf(km, confine_infinities(kx[1]));
+    }
+    const uint16_t vbits = (uint16_t)vmax;
+    float vm = to_float(*reinterpret_cast<const T*>(&vbits));
+    if (odd) {
+      vm = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float2 x[8];
+        widen8<T>(wa[c], x);
+        widen8<T>(wb[c], x + 4);
+        if (live[c]) vm = fmaxf(vm, confine_infinities(x));
+      }
+    }
+    const uint32_t kt_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(km));
+    const uint32_t vt_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(vm));
+    const int next = turn_no == 2 ? 0 : turn_no + 1;
+    if ((tid & 31) == 0) {
+      atomicMax(&s_top[turn_no][team][0], kt_bits);
+      atomicMax(&s_top[turn_no][team][1], vt_bits);
+    }
+    if (tt < 2) s_top[next][team][tt] = 0;
+    const size_t sc = (size_t)u.id * st.Hkv + (on ? head : h_begin);
+    float old_k = 0.f, old_v = 0.f;
+    if (u.slot0 > 0) {
+      old_k = st.k_scale[sc];
+      old_v = st.v_scale[sc];
+    }
+    __syncthreads();  // every thread has read the old scales and written its maximum
+    km = __uint_as_float(s_top[turn_no][team][0]);
+    vm = __uint_as_float(s_top[turn_no][team][1]);
+    turn_no = next;
+    if (!on) continue;
+    const float new_k = grown(old_k, km), new_v = grown(old_v, vm);
+    if (tt == 0) {
+      st.k_scale[sc] = new_k;
+      st.v_scale[sc] = new_v;
+    }
+    const float inv_k = inverse(new_k), inv_v = inverse(new_v);
+    uint8_t* kp = st.k_pages + (sc * D << p.log_page);
+    uint8_t* vp = st.v_pages + (sc * D << p.log_page);
+    if (u.slot0 > 0) {
+      if (old_k > 0.f && new_k > old_k) reexpress<D>(kp, u.slot0, old_k * inv_k, tt, 1 << log_team);
+      if (old_v > 0.f && new_v > old_v) reexpress<D>(vp, u.slot0, old_v * inv_v, tt, 1 << log_team);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (live[c]) {
+        const int at = (slot + c * (P / 2)) * D;
+        *reinterpret_cast<uint2*>(kp + at + it.e0) = quantised(kx[c], inv_k);
+        *reinterpret_cast<uint2*>(kp + at + it.e1) = quantised(kx[c] + 4, inv_k);
+        *reinterpret_cast<uint4*>(vp + at + 16 * j) = quantised_packed<T>(wa[c], wb[c], inv_v, odd);
+      }
+  }
+}
+
+// ------------------------------------------------------------------ few rows per page
+// A warp per (page, head), four heads per CTA; 512 / D rows at a time. One round keeps its rows in
+// registers; more rows are read twice, for the maximum and for the store.
+template <typename T, int D, bool PAIRED>
+__global__ void __launch_bounds__(128) paged_append_rows_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int IPR = D / 16, ROWS = 32 / IPR;  // items per row, rows per round
+  __shared__ __align__(16) float2 s_cs[ROWS * (D / 2)];
+  const SepPagedState& st = p.st;
+  const int P = 1 << p.log_page, tid = threadIdx.x, lane = tid & 31;
+  const int head = blockIdx.y * 4 + (tid >> 5);
+  const bool on = head < st.Hkv;
+  const int h = st.rope.d_rot >> 1, lr = lane / IPR, j = lane % IPR;
+  const Item it = item_of<PAIRED>(st.rope, j);
+  grid_dep_wait();
+  grid_dep_launch_next();
+  Unit u;
+  if (!find_unit(p, blockIdx.x, &u)) return;
+  const size_t sc = (size_t)u.id * st.Hkv + (on ? head : 0);
+  const float old_k = u.slot0 > 0 ? st.k_scale[sc] : 0.f;
+  const float old_v = u.slot0 > 0 ? st.v_scale[sc] : 0.f;
+  if (blockIdx.y == 0)
+    for (int r = tid; r < u.nrow; r += 128)
+      st.flags[(size_t)u.id * P + u.slot0 + r] = p.sep ? p.sep[u.tok0 + r] : 0;
+
+  float2 kx[8];
+  uint4 va, vb;
+  bool odd;
+  float vtop;
+  // rows base .. base + ROWS - 1 of the unit into kx, va, vb (zeros where there is none)
+  auto round = [&](int base) {
+    const int row = base + lr;
+    const bool live = on && row < u.nrow;
+    uint4 ka = make_uint4(0u, 0u, 0u, 0u), kb = ka;
+    va = vb = ka;
+    const T* k = static_cast<const T*>(p.k) + (u.tok0 + (live ? row : 0)) * p.k_tok + (long long)(on ? head : 0) * p.k_head;
+    const T* v = static_cast<const T*>(p.v) + (u.tok0 + (live ? row : 0)) * p.v_tok + (long long)(on ? head : 0) * p.v_head;
+    if (live) {
+      ka = *reinterpret_cast<const uint4*>(k + it.e0);
+      kb = *reinterpret_cast<const uint4*>(k + it.e1);
+      va = *reinterpret_cast<const uint4*>(v + 16 * j);
+      vb = *reinterpret_cast<const uint4*>(v + 16 * j + 8);
+    }
+    __syncthreads();  // the last round's table has been read
+    angle_table(s_cs, min(ROWS, u.nrow - base), h, st.rope.freq, st.rope.magnitude, st.rope.magnitude, tid, 128,
+                [&](int r) { return (double)(u.r0 + base + r); });
+    __syncthreads();
+    if (live) {
+      turn<T, PAIRED>(st.rope, it, ka, kb, k, s_cs + lr * h, kx);
+    } else {
+#pragma unroll
+      for (int z = 0; z < 8; ++z) kx[z] = make_float2(0.f, 0.f);
+    }
+    vtop = largest_packed<T>(va, vb, &odd);
+  };
+  float km = 0.f, vm = 0.f;
+  for (int base = 0; base < u.nrow; base += ROWS) {
+    round(base);
+    km = fmaxf(km, largest(kx));
+    vm = fmaxf(vm, vtop);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+  }
+  const float new_k = grown(old_k, km), new_v = grown(old_v, vm);
+  const float inv_k = inverse(new_k), inv_v = inverse(new_v);
+  uint8_t* kp = st.k_pages + sc * P * D;
+  uint8_t* vp = st.v_pages + sc * P * D;
+  if (on) {
+    if (lane == 0) {
+      st.k_scale[sc] = new_k;
+      st.v_scale[sc] = new_v;
+    }
+    if (old_k > 0.f && new_k > old_k) reexpress<D>(kp, u.slot0, old_k * inv_k, lane, 32);
+    if (old_v > 0.f && new_v > old_v) reexpress<D>(vp, u.slot0, old_v * inv_v, lane, 32);
+  }
+  for (int base = 0; base < u.nrow; base += ROWS) {
+    if (u.nrow > ROWS) round(base);
+    if (!on || base + lr >= u.nrow) continue;
+    const int slot = u.slot0 + base + lr;
+    *reinterpret_cast<uint2*>(kp + slot * D + it.e0) = quantised(kx, inv_k);
+    *reinterpret_cast<uint2*>(kp + slot * D + it.e1) = quantised(kx + 4, inv_k);
+    *reinterpret_cast<uint4*>(vp + slot * D + 16 * j) = quantised_packed<T>(va, vb, inv_v, odd);
+  }
+}
+
+template <typename T, int D, bool PAIRED>
 cudaError_t launch_append_t(AppendParams p, cudaStream_t stream) {
   const int P = p.st.page;
-  const int team = P * D / 8 / kChunks;  // 32 .. 512
-  const int threads = std::max(team, 256), teams = threads / team;
   const long long by_page = p.T / P + 2ll * p.S;
   p.by_token = p.T <= by_page;
-  const long long units = p.by_token ? p.T : by_page;
-  // Few pages: one round of teams per CTA, so that the heads spread over the SMs. Many pages: all
-  // heads of a page in one CTA, which then forms its angle table once.
-  p.heads_per_cta = units >= 148 * 8 ? p.st.Hkv : std::min(teams, p.st.Hkv);
+  if (p.by_token)  // two tokens per sequence at most on average
+    return launch_chained(paged_append_rows_kernel<T, D, PAIRED>, dim3((unsigned)p.T, (p.st.Hkv + 3) / 4), dim3(128), 0,
+                          stream, p);
+  const int team = P * D / 32;  // threads of a head, 32 .. 512
+  const int threads = std::max(team, 256), teams = threads / team;
+  // Four CTAs per SM and more, and otherwise as many heads as possible in one CTA, which
+  // forms its angle table once for all of them.
+  const long long groups = std::min<long long>(p.st.Hkv, (148 * 4 + by_page - 1) / by_page);
+  p.heads_per_cta = std::max(teams, (int)((p.st.Hkv + groups - 1) / groups));
   const size_t smem = (size_t)P * (p.st.rope.d_rot / 2) * sizeof(float2);
   if (smem > 48 * 1024) {
     static std::atomic<bool> set[64];
@@ -286,14 +506,14 @@ cudaError_t launch_append_t(AppendParams p, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !set[dev].load()) {
-      e = cudaFuncSetAttribute(paged_append_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(paged_append_page_kernel<T, D, PAIRED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                128 * (D / 2) * (int)sizeof(float2));
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) set[dev].store(true);
     }
   }
-  const dim3 grid((unsigned)units, (p.st.Hkv + p.heads_per_cta - 1) / p.heads_per_cta);
-  return launch_chained(paged_append_kernel<T, D>, grid, dim3(threads), smem, stream, p);
+  const dim3 grid((unsigned)by_page, (p.st.Hkv + p.heads_per_cta - 1) / p.heads_per_cta);
+  return launch_chained(paged_append_page_kernel<T, D, PAIRED>, grid, dim3(threads), smem, stream, p);
 }
 
 }  // namespace
@@ -319,10 +539,14 @@ cudaError_t launch_paged_append(const SepPagedState& st, int dtype, const void* 
   p.S = S;
   p.max_pages = max_pages;
   p.log_page = 31 - __builtin_clz((unsigned)st.page);
-  if (dtype == SEP_DTYPE_BF16)
-    return st.d == 128 ? launch_append_t<__nv_bfloat16, 128>(p, stream)
-                       : launch_append_t<__nv_bfloat16, 64>(p, stream);
-  return st.d == 128 ? launch_append_t<__half, 128>(p, stream) : launch_append_t<__half, 64>(p, stream);
+  const bool paired = !st.rope.interleaved && st.rope.d_rot % 16 == 0;
+  auto go = [&](auto type) {
+    using T = decltype(type);
+    if (st.d == 128)
+      return paired ? launch_append_t<T, 128, true>(p, stream) : launch_append_t<T, 128, false>(p, stream);
+    return paired ? launch_append_t<T, 64, true>(p, stream) : launch_append_t<T, 64, false>(p, stream);
+  };
+  return dtype == SEP_DTYPE_BF16 ? go(__nv_bfloat16()) : go(__half());
 }
 
 }  // namespace sep

@@ -9,8 +9,11 @@
 //
 // The data is read and written once and nothing else of size moves, so HBM bounds it. The angle of
 // a (token, pair) is shared by every query and key head: a CTA takes a run of tokens with all their
-// heads, forms the (cos, sin) table of its tokens in shared memory (angles in fp64, reduced to
-// [-pi, pi], see rope_angle) and then streams the rows, 16 bytes per access.
+// heads, forms the (cos, sin) table of its tokens in shared memory (angles in fp64,
+// see turn_cos_sin) and then streams the rows, 16 bytes per access. Resident threads, not requests
+// per thread, keep enough bytes in flight: 131072 tokens of 32 + 8 heads of 128 (2.68 GB moved) take 454
+// us at one row per thread and 6 CTAs per SM, 564 us at two rows and 4 CTAs, 717 us at four rows and 2.
+// Steps that only copy need few registers and take four rows at a time.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,7 +27,8 @@ namespace sep {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTokens = 16;  // tokens per CTA
+constexpr int kRopeMaxTokens = 32;  // tokens per CTA
+constexpr int kRopeCtas = 6;        // CTAs per SM
 
 struct RopeSide {
   const void* x;
@@ -42,98 +46,129 @@ struct RopeParams {
   float magnitude, sign;
 };
 
-// One 16-byte (VEC > 1) or one-element access group of a row. A group of the rotated part holds
-// VEC elements and, in the half layout, their partners.
+// One 16-byte (VEC > 1) or one-element access group of a row.
 template <typename T, int VEC>
 struct __align__(sizeof(T) * VEC) Group {
   T v[VEC];
 };
 
+// A row is taken in steps: those that turn (a group and its partners in the half layout, a group of
+// neighbours or one pair when interleaved), and those that copy the rest.
 template <typename T, int VEC, bool INTER>
-__device__ __forceinline__ void rope_row_group(const RopeParams& p, const T* x, T* y, int u,
-                                               const float2* cs) {
+struct Step {
   using Gr = Group<T, VEC>;
-  const int h = p.d_rot >> 1;
-  const int nrot = INTER ? p.d_rot / VEC : h / VEC;  // groups of the rotated part
-  if (VEC > 1 || !INTER) {
-    if (u < nrot) {
-      if (INTER) {
-        Gr a = *reinterpret_cast<const Gr*>(x + u * VEC), r;
+  static constexpr bool kOne = INTER && VEC == 1;                 // pair by pair
+  static constexpr bool kTwo = !INTER || kOne;                    // two groups
+  static constexpr int kWide = INTER && VEC > 1 ? VEC / 2 : VEC;  // pairs of a step
+  int at, at2, pair;  // first elements of the groups, first pair
+  __device__ __forceinline__ Step(const RopeParams& p, int u) {
+    pair = u * kWide;
+    at = INTER ? 2 * pair : pair;
+    at2 = kOne ? at + 1 : pair + (p.d_rot >> 1);
+  }
+  __device__ __forceinline__ void load(const T* x, Gr& a, Gr& b) const {
+    a = *reinterpret_cast<const Gr*>(x + at);
+    if (kTwo) b = *reinterpret_cast<const Gr*>(x + at2);
+  }
+  __device__ __forceinline__ void turn_store(T* y, Gr a, Gr b, const float2* cs) const {
+    if (!kTwo) {
 #pragma unroll
-        for (int z = 0; z + 1 < VEC; z += 2) {
-          const float2 c = cs[(u * VEC + z) >> 1];
-          const float x1 = to_float(a.v[z]), x2 = to_float(a.v[z + 1]);
-          r.v[z] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
-          r.v[z + 1] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
-        }
-        *reinterpret_cast<Gr*>(y + u * VEC) = r;
-      } else {
-        Gr a = *reinterpret_cast<const Gr*>(x + u * VEC);
-        Gr b = *reinterpret_cast<const Gr*>(x + h + u * VEC);
-#pragma unroll
-        for (int z = 0; z < VEC; ++z) {
-          const float2 c = cs[u * VEC + z];
-          const float x1 = to_float(a.v[z]), x2 = to_float(b.v[z]);
-          a.v[z] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
-          b.v[z] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
-        }
-        *reinterpret_cast<Gr*>(y + u * VEC) = a;
-        *reinterpret_cast<Gr*>(y + h + u * VEC) = b;
+      for (int z = 0; z + 1 < VEC; z += 2) {
+        const float2 c = cs[pair + (z >> 1)];
+        const float x1 = to_float(a.v[z]), x2 = to_float(a.v[z + 1]);
+        a.v[z] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
+        a.v[z + 1] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
       }
     } else {
-      const int e = p.d_rot + (u - nrot) * VEC;
-      *reinterpret_cast<Gr*>(y + e) = *reinterpret_cast<const Gr*>(x + e);
+#pragma unroll
+      for (int z = 0; z < VEC; ++z) {
+        const float2 c = cs[pair + z];
+        const float x1 = to_float(a.v[z]), x2 = to_float(b.v[z]);
+        a.v[z] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
+        b.v[z] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
+      }
+      *reinterpret_cast<Gr*>(y + at2) = b;
     }
-  } else {  // interleaved, element by element: a group is one pair, then single elements
-    if (u < h) {
-      const float2 c = cs[u];
-      const float x1 = to_float(x[2 * u]), x2 = to_float(x[2 * u + 1]);
-      y[2 * u] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
-      y[2 * u + 1] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
-    } else {
-      y[p.d_rot + u - h] = x[p.d_rot + u - h];
+    *reinterpret_cast<Gr*>(y + at) = a;
+  }
+};
+
+// Goes over the rows of a CTA's tokens: thread tid takes step tid % U of rows tid / U, + 256 / U, ...,
+// BATCH rows requested together. load(x, k), store(y, tok, k): the step of one row, k its batch slot.
+template <int BATCH, typename T, typename Load, typename Store>
+__device__ __forceinline__ void over_rows(const RopeSide& s, const long long* xo, const long long* yo, int nt, int U,
+                                          int tid, Load load, Store store) {
+  const int rows = nt * s.H, per = kRopeThreads / U, r0 = tid / U;
+  if (r0 >= per) return;
+  // row / H by a product: exact while rows * H < 2^32 (H <= 8192)
+  const unsigned magic = s.H == 1 ? 0u : 0xffffffffu / (unsigned)s.H + 1u;
+  const T* xb = static_cast<const T*>(s.x);
+  T* yb = static_cast<T*>(s.y);
+  for (int row = r0; row < rows; row += per * BATCH) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int x = row + k * per;
+      if (x < rows) {
+        const int tok = s.H == 1 ? x : (int)__umulhi((unsigned)x, magic);
+        load(xb + xo[tok] + (x - tok * s.H) * s.xs[2], k);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int x = row + k * per;
+      if (x < rows) {
+        const int tok = s.H == 1 ? x : (int)__umulhi((unsigned)x, magic);
+        store(yb + yo[tok] + (x - tok * s.H) * s.ys[2], tok, k);
+      }
     }
   }
 }
 
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 s_cs[];  // [tokens][d_rot / 2]
-  __shared__ int s_b[kRopeMaxTokens], s_l[kRopeMaxTokens];
-  const int h = p.d_rot >> 1;
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p) {
+  using St = Step<T, VEC, INTER>;
+  extern __shared__ __align__(16) float2 s_cs[];  // [tokens][d_rot / 2]
+  __shared__ long long s_x[2][kRopeMaxTokens], s_y[2][kRopeMaxTokens], s_pos[kRopeMaxTokens];
+  const int h = p.d_rot >> 1, tid = threadIdx.x;
   const long long t0 = (long long)blockIdx.x * p.tokens;
   const int nt = (int)min((long long)p.tokens, p.ntok - t0);
-  grid_dep_wait();
-  grid_dep_launch_next();
-  if (threadIdx.x < nt) {
-    s_b[threadIdx.x] = (int)((t0 + threadIdx.x) / p.L);
-    s_l[threadIdx.x] = (int)((t0 + threadIdx.x) % p.L);
-  }
-  for (int e = threadIdx.x; e < nt * h; e += kRopeThreads) {
-    const long long t = t0 + e / h;
-    const long long at = (t / p.L) * p.pos_stride + t % p.L;
-    const long long pos = p.pos64 ? static_cast<const long long*>(p.pos)[at]
-                                  : (long long)static_cast<const int*>(p.pos)[at];
-    float c, s;
-    rope_angle(pos, __ldg(p.freq + e % h), &c, &s);
-    s_cs[e] = make_float2(c * p.magnitude, s * p.magnitude * p.sign);
+  if (tid < nt) {
+    const long long b = (t0 + tid) / p.L, l = (t0 + tid) - b * p.L;
+    s_pos[tid] = b * p.pos_stride + l;
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd) {
+      s_x[sd][tid] = b * p.side[sd].xs[0] + l * p.side[sd].xs[1];
+      s_y[sd][tid] = b * p.side[sd].ys[0] + l * p.side[sd].ys[1];
+    }
   }
   __syncthreads();
-  const int nrot = (VEC == 1 || !INTER) ? h / VEC : p.d_rot / VEC;
-  const int U = nrot + (p.copy_rest ? (p.d - p.d_rot) / VEC : 0);
-  const int H = p.side[0].H + p.side[1].H;
-  const int rows = nt * H;
-  const unsigned items = (unsigned)rows * U;
-  for (unsigned i = threadIdx.x; i < items; i += kRopeThreads) {
-    const unsigned row = i / (unsigned)U, u = i - row * U;
-    const unsigned tok = row / (unsigned)H;
-    int head = row - tok * H;
-    const int sd = head >= p.side[0].H;
-    head -= sd ? p.side[0].H : 0;
+  grid_dep_wait();
+  grid_dep_launch_next();
+  angle_table(s_cs, nt, h, p.freq, p.magnitude, p.magnitude * p.sign, tid, kRopeThreads, [&](int r) {
+    return p.pos64 ? (double)static_cast<const long long*>(p.pos)[s_pos[r]]
+                   : (double)static_cast<const int*>(p.pos)[s_pos[r]];
+  });
+  __syncthreads();
+  const int turns = h / St::kWide, copies = p.copy_rest ? (p.d - p.d_rot) / VEC : 0;
+#pragma unroll 1
+  for (int sd = 0; sd < 2; ++sd) {
     const RopeSide& s = p.side[sd];
-    const T* x = static_cast<const T*>(s.x) + s_b[tok] * s.xs[0] + s_l[tok] * s.xs[1] + head * s.xs[2];
-    T* y = static_cast<T*>(s.y) + s_b[tok] * s.ys[0] + s_l[tok] * s.ys[1] + head * s.ys[2];
-    rope_row_group<T, VEC, INTER>(p, x, y, u, s_cs + tok * h);
+    if (s.H == 0) break;
+    {
+      const St st(p, tid % turns);
+      typename St::Gr a, b;
+      over_rows<1, T>(
+          s, s_x[sd], s_y[sd], nt, turns, tid, [&](const T* x, int) { st.load(x, a, b); },
+          [&](T* y, int tok, int) { st.turn_store(y, a, b, s_cs + tok * h); });
+    }
+    for (int c0 = 0; c0 < copies; c0 += kRopeThreads) {  // one round, but for element by element
+      const int n = min(copies - c0, kRopeThreads), at = p.d_rot + (c0 + tid % n) * VEC;
+      typename St::Gr a[4];
+      over_rows<4, T>(
+          s, s_x[sd], s_y[sd], nt, n, tid,
+          [&](const T* x, int k) { a[k] = *reinterpret_cast<const typename St::Gr*>(x + at); },
+          [&](T* y, int, int k) { *reinterpret_cast<typename St::Gr*>(y + at) = a[k]; });
+    }
   }
 }
 
@@ -190,8 +225,8 @@ cudaError_t launch_rope(const SepRope& r, int dtype, int B, int L, int d, const 
   p.copy_rest = !inplace;
   p.magnitude = r.magnitude;
   p.sign = sign;
-  // enough CTAs for every SM a few times over, then up to 16 tokens each
-  p.tokens = (int)std::min<long long>(kRopeMaxTokens, std::max<long long>(1, p.ntok / (148 * 6)));
+  // one wave of CTAs while that gives each up to kRopeMaxTokens tokens
+  p.tokens = (int)std::min<long long>(kRopeMaxTokens, (p.ntok + 148 * kRopeCtas - 1) / (148 * kRopeCtas));
   if (dtype == SEP_DTYPE_BF16) return launch_rope_t<__nv_bfloat16>(p, vec, stream);
   if (dtype == SEP_DTYPE_F16) return launch_rope_t<__half>(p, vec, stream);
   return launch_rope_t<float>(p, vec, stream);

@@ -7,15 +7,32 @@
 
 namespace sep {
 
-// (cos, sin) of the angle pos * f with the arithmetic of SepCache's kernels (k_sepcache.cu), so that
-// a key rotated here and one rotated there agree: the angle is formed in fp64 and reduced to
-// [-pi, pi] by subtracting the nearest multiple of 2 pi (fp64), then the fp32 sincosf of the
-// reduced angle is taken. The error is about 1e-7 absolute, from rounding the reduced angle.
-__device__ __forceinline__ void rope_angle(long long pos, double f, float* cs, float* sn) {
-  constexpr double kTwoPi = 6.283185307179586, kInvTwoPi = 0.15915494309189535;
-  const double x = __dmul_rn((double)pos, f);
-  const double r = __fma_rn(-rint(__dmul_rn(x, kInvTwoPi)), kTwoPi, x);
-  sincosf((float)r, sn, cs);
+// (cos, sin) of the angle pos * f, f given in turns per position: fp64 product, reduced to [-1/2, 1/2]
+// turns, then sincospif in fp32 (whose argument needs no reduction of its own). Rounding the reduced
+// angle to fp32 costs up to pi 2^-24.
+constexpr double kInvTwoPi = 0.15915494309189535;
+__device__ __forceinline__ float2 turn_cos_sin(double pos, double turns) {
+  const double t = __dmul_rn(pos, turns);
+  float2 r;
+  sincospif(2.f * (float)(t - rint(t)), &r.y, &r.x);
+  return r;
+}
+
+// The (cos, sin) table [rows][h] of positions pos_of(0) .. pos_of(rows - 1), by nthr threads: a thread
+// keeps one pair's frequency and goes down the rows. mc, ms: factors of cos and sin.
+template <typename PosOf>
+__device__ __forceinline__ void angle_table(float2* cs, int rows, int h, const double* freq, float mc, float ms,
+                                            int tid, int nthr, PosOf pos_of) {
+  if (h == 0) return;
+  const int per = max(1, nthr / h), r0 = tid / h, z0 = tid - r0 * h;
+  if (r0 >= per) return;
+  for (int z = z0; z < h; z += nthr) {  // one round unless there are more pairs than threads
+    const double turns = __dmul_rn(__ldg(freq + z), kInvTwoPi);
+    for (int r = r0; r < rows; r += per) {
+      const float2 c = turn_cos_sin(pos_of(r), turns);
+      cs[r * h + z] = make_float2(c.x * mc, c.y * ms);
+    }
+  }
 }
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
