@@ -411,7 +411,7 @@ int seppaged_append(const SepPagedState* st, int dtype, const void* k, int64_t k
  * prompt's chunk); the tokens' own keys must have been appended.
  * q [T, Hq, d] bf16 or fp16, already rotated, element strides for token and head, multiples of 8;
  * o [T, Hq, d] contiguous, of q's type; lse [T, Hq] fp32 (NULL: not written). Hq % Hkv == 0,
- * S <= 4096, T * Hq < 2^31, a >= 0, n >= 0. workspace: 256-byte aligned, of
+ * S <= 4096, T * Hq < 2^31, a >= 0, n >= 0, scale > 0. workspace: 256-byte aligned, of
  * seppaged_attn_workspace_size(S, d) bytes, needs no initialisation and carries nothing from one
  * call to the next; calls that may overlap in time (graphs on two streams) need one each.
  */

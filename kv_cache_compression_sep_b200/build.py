@@ -20,8 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsepattn.so")
 SOURCES = ["k_mask.cu", "k_attn_fwd.cu", "k_attn_bwd.cu", "k_sepcache.cu", "k_scratch.cu",
-           "k_rope.cu", "k_paged_append.cu", "k_paged_attn.cu", "api.cpp"]
-HEADERS = ["sep_common.cuh", "sep_rope.cuh", "sep_tiles.cuh", "sep_launch.h"]
+           "k_rope.cu", "k_paged_append.cu", "k_paged_attn.cu", "k_paged_chunk.cu",
+           "api.cpp"]
+HEADERS = ["sep_common.cuh", "sep_paged.cuh", "sep_rope.cuh", "sep_tiles.cuh", "sep_launch.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include")]
 

@@ -392,7 +392,9 @@ int seppaged_attn(const SepPagedState* st, int dtype, const void* q, int64_t q_t
                   size_t workspace_bytes, sep_stream_t stream) {
   int e = check_paged(st, dtype, T, S, max_pages, page_table, seq_lens, indptr);
   if (e != SEP_OK) return e;
-  if (!q || !o || Hq < 1 || Hq % st->Hkv != 0 || a < 0 || n < 0) return SEP_ERR_INVALID_ARG;
+  if (!q || !o || Hq < 1 || Hq % st->Hkv != 0 || a < 0 || n < 0 || !(scale > 0.f) ||
+      scale > 3.4e38f)
+    return SEP_ERR_INVALID_ARG;
   if (S > 4096 || (long long)T * Hq > 2147483647ll) return SEP_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(o) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0)
     return SEP_ERR_MISALIGNED;

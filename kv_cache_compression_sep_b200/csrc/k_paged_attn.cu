@@ -24,7 +24,7 @@
 // Work split: every (sequence, KV head, row tile) has a number of key tiles, all tiles of the call
 // are numbered in a row, and each warp takes an equal run of them, wherever sequences begin and
 // end. A warp that covers all tiles of a row tile writes the result; otherwise it leaves its part
-// in the workspace and seppaged_join_kernel adds the parts in the order of the warps (same bits
+// in the workspace and paged_join_kernel adds the parts in the order of the warps (same bits
 // every time).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,7 +34,7 @@
 
 #include "sep_common.cuh"
 #include "sep_launch.h"
-#include "sep_rope.cuh"
+#include "sep_paged.cuh"
 
 namespace sep {
 
@@ -48,41 +48,6 @@ constexpr int kScan = 256;           // positions of a tile left of the window (
 constexpr int kDense = 64;           // positions of a window tile (every row loaded)
 constexpr int kMaxWarps = 2048;      // workspace slots are laid out for this many
 
-struct PagedAttnParams {
-  const uint8_t *k_pages, *v_pages;
-  const float *k_scale, *v_scale;
-  const uint8_t* flags;
-  const void* q;
-  long long q_tok, q_head;
-  void* o;
-  float* lse;
-  const int32_t *table, *lens, *indptr;
-  long long* base;  // [S + 1] first tile of each sequence (workspace)
-  float* part;      // parts of row tiles that several warps share (workspace)
-  unsigned* err;
-  int T, S, Hq, Hkv, G, num_pages, max_pages, log_page, a, n, bf16, nwarps;
-  float scale_log2;
-};
-
-// ------------------------------------------------------------------ tiles of a sequence
-struct SeqInfo {
-  int len;       // tokens in the pages that may be read
-  int tok0, nq;  // first query token and count
-  int lead;      // position of query 0 (negative: padding queries, which keep nothing)
-  bool bad;      // an index was out of range
-};
-constexpr int kMaxLen = 1 << 30;
-__device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int s) {
-  SeqInfo q;
-  const int i0 = __ldg(p.indptr + s), i1 = __ldg(p.indptr + s + 1);
-  q.tok0 = max(0, min(i0, p.T));
-  q.nq = max(0, min(i1, p.T) - q.tok0);
-  const int len = __ldg(p.lens + s);
-  q.len = (int)min((long long)min(max(len, 0), kMaxLen), (long long)p.max_pages << p.log_page);
-  q.lead = q.len - q.nq;
-  q.bad = i0 != q.tok0 || i1 != q.tok0 + q.nq || len != q.len;
-  return q;
-}
 // Row tile rt covers rows rt * R .. of the sequence's nq * G (token, head in group) rows.
 struct RowTile {
   int w0, kend;  // keys [w0, kend) are loaded whole, keys [0, w0) only where kept by every row
@@ -108,20 +73,11 @@ __device__ __forceinline__ int tiles_per_row_tile(const PagedAttnParams& p, cons
   return min(all, (int)win + (last_w0 + kScan - 1) / kScan);
 }
 __device__ __forceinline__ int row_tiles(const PagedAttnParams& p, const SeqInfo& q, int R) {
+  if (is_chunk(p, q)) return 0;
   return (int)(((long long)q.nq * p.G + R - 1) / R);
 }
 
 // ------------------------------------------------------------------ fragments
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t w) {  // low 16 bits: two e4m3 -> two fp16
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t cvt_e4m3x2_hi(uint32_t w) {  // high 16 bits
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -135,27 +91,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Byte masks of the NaN bytes (0x7f, 0xff) of four e4m3 values: 0x80 in each such byte.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
-constexpr uint32_t kNoRow = 0xffffffffu;
-
-// The exponent fields of a page's scales (powers of two, or 0 while the page holds only zeros), and the
-// key scale and the log2 of the value scale (-inf for 0) from them.
-__device__ __forceinline__ uint32_t scale_exponents(float ks, float vs) {
-  return (__float_as_uint(ks) >> 23 & 0xffu) | (__float_as_uint(vs) >> 23 & 0xffu) << 8;
-}
-__device__ __forceinline__ float key_scale(uint32_t ex) { return __uint_as_float((ex & 0xffu) << 23); }
-__device__ __forceinline__ float value_log2(uint32_t ex) {
-  return ex >> 8 ? (float)((int)(ex >> 8) - 127) : -INFINITY;
-}
-
 // A stage of a warp's ring: 32 key rows, then 32 value rows, D bytes each, in 16-byte pieces. Piece c of
 // row r lies at piece c ^ swz(r), so that the fragment reads (several rows at one piece) and the copies
 // (whole rows) both touch every bank once (D = 64: values twice).
@@ -440,19 +375,12 @@ __device__ __forceinline__ void begin_rows(const PagedAttnParams& p, RowState<D,
   }
 }
 
-__device__ __forceinline__ void store_out(const PagedAttnParams& p, long long at, float a, float b) {
-  uint32_t w;
-  if (p.bf16) w = pack_bf16x2(a, b);
-  else w = pack_half2(a, b);
-  *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at) = w;
-}
 // acc * 2^(mo - m) / l: the exponent split in two, so that neither factor leaves fp32 where their
 // product does not
 __device__ __forceinline__ float2 join_factors(float mo, float m, float l) {
   const float x = mo - m, h = rintf(0.5f * x);
   return make_float2(ex2(h), ex2(x - h) / l);
 }
-constexpr float kLn2 = 0.69314718055994531f;
 
 // Part of a row tile in the workspace: [R][D] accumulators, then [R][4] of mo, m, l.
 template <int D, int R>
@@ -827,36 +755,25 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
 }
 
 // ------------------------------------------------------------------ join of the parts
-// One CTA per (query token, query head). Its row tile's tiles belong to warps w0 .. w1; with w0 = w1
-// the row is written already. Part of warp w0 is in its slot 1 unless its run begins with this row
-// tile; the others begin with it (slot 0). The factors of all parts come first, in shared memory; the
-// accumulators are then added in the order of the warps, kJoinGroups interleaved sums.
+// The tiles of a row tile belong to warps w0 .. w1; with w0 = w1 its rows are written already. Part of
+// warp w0 is in its slot 1 unless its run begins with this row tile; the others begin with it (slot 0).
+// The factors of all parts come first, in shared memory; the accumulators are then added in the order of
+// the warps, in interleaved sums.
 constexpr int kJoinThreads = 256;
+template <int D>
+struct JoinShared {
+  static constexpr int LPR = D / 4, GR = kJoinThreads / LPR;  // lanes per row, groups of lanes
+  float4 acc[GR][LPR];
+  float f[kMaxWarps];
+  float red[3][kJoinThreads / 32];
+};
+// Row `row` of a sequence and KV head, by the whole CTA; its row tile's tiles are t0 .. t1 - 1.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) seppaged_join_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int R = 8 * NT, LPR = D / 4, GR = kJoinThreads / LPR;  // lanes per row, groups of lanes
-  __shared__ float4 s_acc[GR][LPR];
-  __shared__ float s_f[kMaxWarps];
-  __shared__ float s_red[3][kJoinThreads / 32];
-  grid_dep_wait();
-  grid_dep_launch_next();
-  const int tok = blockIdx.x / p.Hq, hq = blockIdx.x - tok * p.Hq;
+__device__ __forceinline__ void join_row(const PagedAttnParams& p, JoinShared<D>& sh, const SeqInfo& q, int h, int row,
+                                         long long t0, long long t1, long long per) {
+  constexpr int R = 8 * NT, LPR = JoinShared<D>::LPR, GR = JoinShared<D>::GR;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // sequence of the token: last s with indptr[s] <= tok
-  int seq = -1;
-  for (int s0 = 0; s0 < p.S; s0 += kJoinThreads) {
-    const int hit = __syncthreads_count(s0 + tid < p.S && __ldg(p.indptr + s0 + tid) <= tok);
-    seq += hit;
-    if (hit < min(kJoinThreads, p.S - s0)) break;
-  }
-  if (seq < 0) return;
-  const SeqInfo q = seq_info(p, seq);
-  if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
-  const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
-  const int rt = row / R, lr = row - rt * R;
-  const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
-  const long long t0 = p.base[seq] + ((long long)h * nrt + rt) * per_rt, t1 = t0 + per_rt;
-  const long long per = (p.base[p.S] + p.nwarps - 1) / p.nwarps;
+  const int lr = row % R, tok = q.tok0 + row / p.G, hq = h * p.G + row % p.G;
   const int w0 = (int)(t0 / per), w1 = (int)((t1 - 1) / per), parts = w1 - w0 + 1;
   if (parts == 1) return;
   const int first_slot = t0 > (long long)w0 * per ? 1 : 0;
@@ -874,51 +791,51 @@ __global__ void __launch_bounds__(kJoinThreads) seppaged_join_kernel(const __gri
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
   if (lane == 0) {
-    s_red[0][warp] = mo;
-    s_red[1][warp] = m;
+    sh.red[0][warp] = mo;
+    sh.red[1][warp] = m;
   }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) {
-    mo = fmaxf(mo, s_red[0][w]);
-    m = fmaxf(m, s_red[1][w]);
+    mo = fmaxf(mo, sh.red[0][w]);
+    m = fmaxf(m, sh.red[1][w]);
   }
   const float mor = mo == -INFINITY ? 0.f : mo, mr = m == -INFINITY ? 0.f : m;
   // ---- factors of the parts and the row sum
   float l = 0.f;
   for (int i = tid; i < parts; i += kJoinThreads) {
     const float4 st = *reinterpret_cast<const float4*>(part(i) + (size_t)R * D + lr * 4);
-    s_f[i] = ex2(st.x - mor);
+    sh.f[i] = ex2(st.x - mor);
     l += st.z * ex2(st.y - mr);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) s_red[2][warp] = l;
+  if (lane == 0) sh.red[2][warp] = l;
   __syncthreads();
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[2][w];
+  for (int w = 0; w < kJoinThreads / 32; ++w) l += sh.red[2][w];
   // ---- accumulators
   const int grp = tid / LPR, c = tid - grp * LPR;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = grp; i < parts; i += GR) {
     const float4 a = *reinterpret_cast<const float4*>(part(i) + (size_t)lr * D + c * 4);
-    const float f = s_f[i];
+    const float f = sh.f[i];
     acc.x = fmaf(a.x, f, acc.x);
     acc.y = fmaf(a.y, f, acc.y);
     acc.z = fmaf(a.z, f, acc.z);
     acc.w = fmaf(a.w, f, acc.w);
   }
-  s_acc[grp][c] = acc;
+  sh.acc[grp][c] = acc;
   __syncthreads();
-  if (grp != 0) return;
+  if (grp == 0) {
 #pragma unroll
   for (int x = 1; x < GR; ++x) {
-    acc.x += s_acc[x][c].x;
-    acc.y += s_acc[x][c].y;
-    acc.z += s_acc[x][c].z;
-    acc.w += s_acc[x][c].w;
+    acc.x += sh.acc[x][c].x;
+    acc.y += sh.acc[x][c].y;
+    acc.z += sh.acc[x][c].z;
+    acc.w += sh.acc[x][c].w;
   }
   const bool none = m == -INFINITY && !(l != l);
   float2 f = join_factors(mo, m, l);
@@ -927,6 +844,54 @@ __global__ void __launch_bounds__(kJoinThreads) seppaged_join_kernel(const __gri
   store_out(p, at, none ? 0.f : acc.x * f.x * f.y, none ? 0.f : acc.y * f.x * f.y);
   store_out(p, at + 2, none ? 0.f : acc.z * f.x * f.y, none ? 0.f : acc.w * f.x * f.y);
   if (c == 0 && p.lse) p.lse[(long long)tok * p.Hq + hq] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+// One CTA per (query token, query head); where chunks are present (and most tokens belong to them), one
+// per boundary between two warps' runs, for the row tile that it cuts first.
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int R = 8 * NT;
+  __shared__ JoinShared<D> sh;
+  grid_dep_wait();
+  grid_dep_launch_next();
+  const int tid = threadIdx.x;
+  if (p.chunks) {
+    const long long total = p.base[p.S], per = (total + p.nwarps - 1) / p.nwarps;
+    const long long x = (blockIdx.x + 1ll) * per;
+    if (x >= total) return;
+    int lo = 0, hi = p.S;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.base[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    const SeqInfo q = seq_info(p, lo);
+    const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+    const long long unit = (x - p.base[lo]) / per_rt, t0 = p.base[lo] + unit * per_rt;
+    if (t0 == x || t0 / per != blockIdx.x) return;
+    const int h = (int)(unit / nrt), rt = (int)(unit - (long long)h * nrt);
+    for (int row = rt * R; row < min(rt * R + R, q.nq * p.G); ++row) {
+      join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, per);
+      __syncthreads();
+    }
+    return;
+  }
+  const int tok = blockIdx.x / p.Hq, hq = blockIdx.x - tok * p.Hq;
+  // sequence of the token: last s with indptr[s] <= tok
+  int seq = -1;
+  for (int s0 = 0; s0 < p.S; s0 += kJoinThreads) {
+    const int hit = __syncthreads_count(s0 + tid < p.S && __ldg(p.indptr + s0 + tid) <= tok);
+    seq += hit;
+    if (hit < min(kJoinThreads, p.S - s0)) break;
+  }
+  if (seq < 0) return;
+  const SeqInfo q = seq_info(p, seq);
+  if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
+  const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
+  const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+  const long long t0 = p.base[seq] + ((long long)h * nrt + row / R) * per_rt;
+  join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, (p.base[p.S] + p.nwarps - 1) / p.nwarps);
 }
 
 template <int D, int NT>
@@ -949,7 +914,8 @@ cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
   p.nwarps = grid * kWarps;
   e = launch_chained(paged_attn_kernel<D, NT>, dim3(grid), dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(seppaged_join_kernel<D, NT>, dim3((unsigned)p.T * p.Hq), dim3(kJoinThreads), 0, stream, p);
+  return launch_chained(paged_join_kernel<D, NT>, dim3(p.chunks ? (unsigned)p.nwarps : (unsigned)p.T * p.Hq),
+                        dim3(kJoinThreads), 0, stream, p);
 }
 
 }  // namespace
@@ -996,6 +962,13 @@ cudaError_t launch_paged_attn(const SepPagedState& st, int dtype, const void* q,
   // 16-row tiles once the sequences have more than 8 (token, head) rows on average: keys are then
   // converted once for 16 rows instead of 8
   const bool wide = (long long)T * p.G > 8ll * S;
+  // Sequences with many rows go to tcgen05 tiles of 128 rows. The host knows averages only: up to 16 rows
+  // per sequence on average everything stays here.
+  p.chunks = (long long)T * p.G > 16ll * S;
+  if (p.chunks) {
+    const cudaError_t e = launch_paged_chunks(p, st.d, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (st.d == 128)
     return wide ? launch_paged_attn_t<128, 2>(p, stream) : launch_paged_attn_t<128, 1>(p, stream);
   return wide ? launch_paged_attn_t<64, 2>(p, stream) : launch_paged_attn_t<64, 1>(p, stream);

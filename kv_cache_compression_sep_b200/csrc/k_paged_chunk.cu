@@ -1,0 +1,713 @@
+// seppaged_attn for chunks: sequences with many query rows, on tcgen05.
+//
+// The mathematics is that of k_paged_attn.cu; here the products bound the call (4 d flops per kept
+// pair), so the stored numbers are turned into fp16 operands in shared memory once for 256 query rows:
+// one CTA takes two tiles of 128 (token, head in group) rows of one KV head. For 128 keys at a time
+//   S_w = Q_w K^T       (tcgen05.mma, fp16 operands K-major in shared memory, fp32 in TMEM)
+//   P_w = 2^(S_w c - m) (one thread per row: running maximum, lazily rescaled sums, fp16 P into the
+//                        upper half of S_w's columns)
+//   O_w += P_w V        (A from TMEM, V MN-major in shared memory)
+// for w = 0, 1 in turn, so that the tensor cores work on one row tile while the softmax is in the other.
+// Warps 0-3 and 4-7: softmax of row tiles 0 and 1; warps 8-11: keys and values; warp 12: MMA issue.
+//
+// Operands. q as fp16 times a power of two per row (exact for bf16 above 2^-28 of the row's largest).
+// Keys and values as fp16 relative to the largest scale of the sequence's pages (one power of two for K
+// and one for V, per sequence and KV head): exact while a page's scale is within 2^15 of that, and
+// otherwise rounded to 2^-25 of it, 2^-33 of the largest magnitude. The weights are rounded to fp16.
+//
+// Keys left of every row's window are gathered: the converter warps list positions that are initial
+// or flagged and read their rows 128 at a time, like window tiles. A NaN among the values is taken as 0 in
+// the product and brought back at the end in the rows that keep its key (rows that do not must not
+// see it, and 0 * NaN would tell them).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "sep_common.cuh"
+#include "sep_launch.h"
+#include "sep_paged.cuh"
+#include "sep_tiles.cuh"
+
+namespace sep {
+
+namespace {
+
+constexpr int kRowsPerItem = 256;
+constexpr int kScanStep = 1024;  // positions examined per refill of the list
+
+struct __align__(8) KeyRow {
+  uint32_t row, ex;  // pool row (kNoRow: none), exponent fields of its page's scales
+};
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int KB = D / 64;                // 128-byte column boxes per row
+  static constexpr int BOX = 128 * 128;            // bytes of one [128 rows][64 fp16] box
+  static constexpr int TILE = KB * BOX;
+  static constexpr int NST = 2;
+  static constexpr int SMEM_TILES = TILE * (2 + 2 * NST);  // Q x 2, NST x (K, V)
+  static constexpr int COL_S = 0, COL_P = 64, COL_O = 256;  // S_w: 128 w; P_w: + 64; O_w: 256 + D w
+  static constexpr int THREADS = 416;
+};
+
+struct TileDesc {
+  int k0;          // first position of a window tile, -1: listed keys
+  int last;        // of the item
+  uint32_t valid[4];  // keys that exist
+  uint32_t anchor[4]; // initial or flagged (window tiles that some row's window does not cover)
+};
+struct ChunkBar {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2], p_ready[2], pv_done[2];
+  uint64_t conv, drain;
+  TileDesc desc[4];
+  KeyRow keys[2][128];
+  // By item modulo 4 (an item's first tile waits for the products of three tiles before, so its slot has
+  // been read by then): exponent fields of the largest scales, a NaN among the values.
+  int ex_k[4], ex_v[4], nan[4];
+  int red[4], part4[4];
+  long long part[13];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr int kListCap = 128 + kScanStep;
+
+template <int D>
+constexpr size_t chunk_smem_bytes(int S) {
+  return 1024 + ChunkCfg<D>::SMEM_TILES + sizeof(KeyRow) * kListCap + sizeof(ChunkBar) + sizeof(int) * (S + 2);
+}
+
+// Work item: 256 rows of one sequence and KV head.
+struct Item {
+  SeqInfo q;
+  int seq, h, r0, rows;  // first row, rows of the sequence
+  int w0, kend;          // window keys [w0, kend); listed keys left of w0
+};
+__device__ __forceinline__ int chunk_items(const PagedAttnParams& p, const SeqInfo& q) {
+  if (!is_chunk(p, q)) return 0;
+  return p.Hkv * (int)(((long long)q.nq * p.G + kRowsPerItem - 1) / kRowsPerItem);
+}
+// Item x of the numbering in `base`; within a sequence the latest (longest) rows first.
+__device__ __forceinline__ Item chunk_item(const PagedAttnParams& p, const int* base, int x) {
+  Item it;
+  int lo = 0, hi = p.S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (base[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  it.seq = lo;
+  it.q = seq_info(p, lo);
+  it.rows = it.q.nq * p.G;
+  const int nrt = (it.rows + kRowsPerItem - 1) / kRowsPerItem, y = x - base[lo];
+  const int rt = nrt - 1 - y / p.Hkv;
+  it.h = y % p.Hkv;
+  it.r0 = rt * kRowsPerItem;
+  const int lo_pos = max(0, it.q.lead + it.r0 / p.G);
+  const int hi_pos = it.q.lead + min(it.q.nq - 1, (it.r0 + kRowsPerItem - 1) / p.G);
+  it.kend = max(0, hi_pos + 1);
+  it.w0 = min(max(0, lo_pos - max(p.n, 1) + 1), it.kend) & ~127;
+  return it;
+}
+
+__host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4)  // D f32; A and B f16 (format 0)
+         | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Four e4m3 numbers as fp16 times f * f2 (powers of two).
+__device__ __forceinline__ uint2 widen4(uint32_t w, __half2 f, __half2 f2, bool far) {
+  uint32_t lo = cvt_e4m3x2(w), hi = cvt_e4m3x2_hi(w);
+  __half2 a = __hmul2(*reinterpret_cast<__half2*>(&lo), f), b = __hmul2(*reinterpret_cast<__half2*>(&hi), f);
+  if (far) {
+    a = __hmul2(a, f2);
+    b = __hmul2(b, f2);
+  }
+  return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+// 2^e as fp16, e in [-24, 0]
+__device__ __forceinline__ __half2 half_pow2(int e) {
+  const uint16_t b = e >= -14 ? (uint16_t)((e + 15) << 10) : (uint16_t)(1u << (e + 24));
+  const __half h = *reinterpret_cast<const __half*>(&b);
+  return __half2half2(h);
+}
+// Factors of a page whose scale has exponent field ex against the largest's, top. Beyond 2^-48 every
+// number rounds to 0.
+struct Shift {
+  __half2 f, f2;
+  bool far;
+};
+__device__ __forceinline__ Shift shift_of(int ex, int top) {
+  const int e = ex == 0 ? 0 : max(ex - top, -48);  // a page of zeros: any factor
+  Shift s;
+  s.far = e < -24;
+  s.f = half_pow2(max(e, -24));
+  s.f2 = half_pow2(max(min(e + 24, 0), -24));
+  return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ PagedAttnParams p) {
+  using C = ChunkCfg<D>;
+  constexpr int NST = C::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;  // two row tiles
+  uint8_t* sK = sQ + 2 * C::TILE;
+  uint8_t* sV = sK + NST * C::TILE;
+  KeyRow* list = reinterpret_cast<KeyRow*>(sV + NST * C::TILE);
+  ChunkBar* bar = reinterpret_cast<ChunkBar*>(list + kListCap);
+  int* base = reinterpret_cast<int*>(bar + 1);  // [S + 1] first item of each sequence
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &bar->abort_flag;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->k_full[s], 128);
+      mbar_init(&bar->k_empty[s], 1);
+      mbar_init(&bar->v_full[s], 128);
+      mbar_init(&bar->v_empty[s], 1);
+      mbar_init(&bar->q_full[s], 128);
+      mbar_init(&bar->s_full[s], 1);
+      mbar_init(&bar->p_ready[s], 128);
+      mbar_init(&bar->pv_done[s], 1);
+    }
+    mbar_init(&bar->conv, 128);
+    mbar_init(&bar->drain, 1);
+    bar->abort_flag = 0;
+    fence_barrier_init();
+  }
+  grid_dep_wait();
+  grid_dep_launch_next();
+  // ---- first item of every sequence
+  int carry = 0;
+  __syncthreads();
+  for (int s0 = 0; s0 < p.S; s0 += C::THREADS) {
+    const int s = s0 + tid;
+    const int x = s < p.S ? chunk_items(p, seq_info(p, s)) : 0;
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) bar->part[warp] = inc;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      if (w < warp) before += (int)bar->part[w];
+      carry += (int)bar->part[w];
+    }
+    if (s < p.S) base[s] = before + inc - x;
+    __syncthreads();
+  }
+  const int nitems = carry;
+  if (tid == 0) base[p.S] = nitems;
+  if ((int)blockIdx.x >= nitems) return;  // no tensor memory was taken
+  if (warp == 12) {
+    tmem_alloc(&bar->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ keys and values
+    const int t = tid - 256;  // key of the tile
+    const int cw = warp - 8;
+    bool ok = true;
+    int syncs = 0;
+    // barrier of the 128 converter threads, bounded like every other wait
+    auto conv_sync = [&]() -> bool {
+      mbar_arrive(&bar->conv);
+      const bool r = __all_sync(0xffffffffu, mbar_wait(&bar->conv, syncs & 1, p.err, abort_flag));
+      ++syncs;
+      return r;
+    };
+    int g = 0, slot = 0;
+    for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
+      const Item it = chunk_item(p, base, x);
+      const int32_t* table = p.table + (long long)it.seq * p.max_pages;
+      // ---- largest scales of the item's pages
+      const int npages = (it.kend + (1 << p.log_page) - 1) >> p.log_page;
+      int ek = 0, ev = 0;
+      for (int pg = t; pg < npages; pg += 128) {
+        const int id = __ldg(table + pg);
+        if (id >= 0 && id < p.num_pages) {
+          const size_t sc = (size_t)id * p.Hkv + it.h;
+          ek = max(ek, (int)(__float_as_uint(__ldg(p.k_scale + sc)) >> 23 & 0xffu));
+          ev = max(ev, (int)(__float_as_uint(__ldg(p.v_scale + sc)) >> 23 & 0xffu));
+        } else {
+          record_failure(p.err, nullptr, SEP_ERR_INDEX);
+        }
+      }
+      ek = __reduce_max_sync(0xffffffffu, ek);
+      ev = __reduce_max_sync(0xffffffffu, ev);
+      if (lane == 0) bar->red[cw] = ek << 16 | ev;
+      if (!(ok = conv_sync())) break;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        ek = max(ek, bar->red[w] >> 16);
+        ev = max(ev, bar->red[w] & 0xffff);
+      }
+      if (t == 0) {
+        bar->ex_k[slot] = ek;
+        bar->ex_v[slot] = ev;
+        bar->nan[slot] = 0;
+      }
+      // ---- the tiles: listed keys, then the window
+      int list_at = 0, list_n = 0, scan = 0, win = it.w0;
+      bool any = false;
+      KeyRow e;        // this thread's key of the next tile
+      int e_k0;        // its window position, -1 listed, -2 no further tile
+      bool e_anchor;
+      auto next_tile = [&]() -> bool {
+        e = KeyRow{kNoRow, 0};
+        e_anchor = false;
+        while (list_n - list_at < 128 && scan < it.w0) {
+          // what is left moves to the front, then kScanStep more positions are examined, 8 per thread
+          const int rem = list_n - list_at;
+          const KeyRow keep = t < rem ? list[list_at + t] : KeyRow{0, 0};
+          const int j0 = scan + 8 * t;
+          uint32_t bits = 0;
+          KeyRow first = {0, 0};
+          if (j0 < it.w0) {
+            const int id = __ldg(table + (j0 >> p.log_page));
+            if (id >= 0 && id < p.num_pages) {
+              const int off = j0 & ((1 << p.log_page) - 1);
+              const uint2 f = __ldg(reinterpret_cast<const uint2*>(p.flags + ((size_t)id << p.log_page) + off));
+#pragma unroll
+              for (int b = 0; b < 8; ++b) bits |= (((b < 4 ? f.x : f.y) >> (8 * (b & 3))) & 0xffu ? 1u : 0u) << b;
+              const int init = p.a - j0;
+              if (init > 0) bits |= init >= 8 ? 0xffu : (1u << init) - 1u;
+              const size_t sc = (size_t)id * p.Hkv + it.h;
+              first.row = (uint32_t)(sc << p.log_page) + off;
+              first.ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
+            }
+          }
+          const int cnt = __popc(bits);
+          int at = cnt;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
+          }
+          if (lane == 31) bar->part4[cw] = at;
+          if (!conv_sync()) return false;
+          at -= cnt;
+          int total = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if (w < cw) at += bar->part4[w];
+            total += bar->part4[w];
+          }
+          if (t < rem) list[t] = keep;
+          at += rem;
+          while (bits) {
+            const int b = __ffs(bits) - 1;
+            bits &= bits - 1;
+            list[at++] = KeyRow{first.row + b, first.ex};
+          }
+          list_at = 0;
+          list_n = rem + total;
+          scan += kScanStep;
+          if (!conv_sync()) return false;
+        }
+        if (list_at < list_n) {
+          if (list_at + t < list_n) e = list[list_at + t];
+          list_at = min(list_at + 128, list_n);
+          e_k0 = -1;
+          any = true;
+          return true;
+        }
+        if (win >= it.kend && any) {
+          e_k0 = -2;
+          return true;
+        }
+        const int j = win + t;
+        if (j < it.kend) {
+          const int id = __ldg(table + (j >> p.log_page));
+          if (id >= 0 && id < p.num_pages) {
+            const size_t sc = (size_t)id * p.Hkv + it.h;
+            const int off = j & ((1 << p.log_page) - 1);
+            e.row = (uint32_t)(sc << p.log_page) + off;
+            e.ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
+            // flags matter where the last row's window does not reach
+            if (it.kend - 1 - win >= p.n)
+              e_anchor = j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + off) != 0;
+          }
+        }
+        e_k0 = win;
+        win += 128;
+        any = true;
+        return true;
+      };
+      if (!(ok = next_tile())) break;
+      for (;;) {
+        const int st = g % NST, rnd = g / NST;
+        const int k0 = e_k0;
+        const uint32_t vmask = __ballot_sync(0xffffffffu, e.row != kNoRow);
+        const uint32_t amask = __ballot_sync(0xffffffffu, e_anchor);
+        bar->keys[g & 1][t] = e;
+        if (!(ok = conv_sync())) break;
+        // ---- this thread's pieces of the tile's rows: 16 numbers of one row at a time
+        constexpr int PPR = D / 16, RPI = 32 / PPR, NI = 32 / RPI;  // pieces per row, rows per load, loads
+        const int piece = lane % PPR;
+        uint4 kx[NI], vx[NI];
+        uint32_t ex[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const KeyRow kr = bar->keys[g & 1][cw * 32 + i * RPI + lane / PPR];
+          kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+          ex[i] = kr.ex;
+          if (kr.row != kNoRow) {
+            kx[i] = __ldg(reinterpret_cast<const uint4*>(p.k_pages + (size_t)kr.row * D + piece * 16));
+            vx[i] = __ldg(reinterpret_cast<const uint4*>(p.v_pages + (size_t)kr.row * D + piece * 16));
+          }
+        }
+        if (!(ok = next_tile())) break;  // its loads go out behind the rows'
+        const bool last = e_k0 == -2;
+        if (rnd > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bar->k_empty[st], (rnd - 1) & 1, p.err, abort_flag)))) break;
+        TileDesc* ds = &bar->desc[g & 3];
+        if (lane == 0) {
+          ds->valid[cw] = vmask;
+          ds->anchor[cw] = amask;
+        }
+        if (t == 0) {
+          ds->k0 = k0;
+          ds->last = last;
+        }
+        auto put = [&](uint8_t* tile, int i, uint4 v, Shift sh) {
+          const int r = cw * 32 + i * RPI + lane / PPR;
+          const uint2 a = widen4(v.x, sh.f, sh.f2, sh.far), b = widen4(v.y, sh.f, sh.f2, sh.far);
+          const uint2 c = widen4(v.z, sh.f, sh.f2, sh.far), d = widen4(v.w, sh.f, sh.f2, sh.far);
+          // elements 16 piece ..: box piece / 4, chunks 2 (piece % 4) and the next; lanes of the second box
+          // store theirs in the other order, so that eight lanes touch every bank once
+          uint8_t* box = tile + (piece >> 2) * C::BOX;
+          const int ch = 2 * (piece & 3);
+          const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
+          const bool swap = piece & 4;
+          *reinterpret_cast<uint4*>(box + sw128_offset(r, ch + (swap ? 1 : 0))) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(box + sw128_offset(r, ch + (swap ? 0 : 1))) = swap ? lo : hi;
+        };
+#pragma unroll
+        for (int i = 0; i < NI; ++i) put(sK + st * C::TILE, i, kx[i], shift_of(ex[i] & 0xff, ek));
+        fence_proxy_async_smem();
+        mbar_arrive(&bar->k_full[st]);
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t n0 = nan_bytes(vx[i].x), n1 = nan_bytes(vx[i].y), n2 = nan_bytes(vx[i].z), n3 = nan_bytes(vx[i].w);
+          if (n0 | n1 | n2 | n3) {
+            bad = 1;
+            vx[i].x &= ~((n0 >> 7) * 0xffu);
+            vx[i].y &= ~((n1 >> 7) * 0xffu);
+            vx[i].z &= ~((n2 >> 7) * 0xffu);
+            vx[i].w &= ~((n3 >> 7) * 0xffu);
+          }
+        }
+        if (bad) *const_cast<volatile int*>(&bar->nan[slot]) = 1;
+        if (rnd > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bar->v_empty[st], (rnd - 1) & 1, p.err, abort_flag)))) break;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) put(sV + st * C::TILE, i, vx[i], shift_of(ex[i] >> 8, ev));
+        fence_proxy_async_smem();
+        mbar_arrive(&bar->v_full[st]);
+        ++g;
+        if (last) break;
+      }
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idS = make_idesc_f16(128, 128, false), idO = make_idesc_f16(128, D, true);
+      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
+      bool ok = true;
+      int g = 0, item = 0;
+      auto issue_S = [&](int w, int gg) {
+        const uint32_t qlo = sdesc_lo(sQa + w * C::TILE, 16), klo = sdesc_lo(sKa + (gg % NST) * C::TILE, 16);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + C::COL_S + w * 128, sdesc_join(qlo + off, kDescHi), sdesc_join(klo + off, kDescHi), idS,
+                 kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bar->s_full[w]);
+      };
+      for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, ++item) {
+        if (!(ok = mbar_wait(&bar->q_full[0], item & 1, p.err, abort_flag))) break;
+        if (!(ok = mbar_wait(&bar->q_full[1], item & 1, p.err, abort_flag))) break;
+        if (!(ok = mbar_wait(&bar->k_full[g % NST], (g / NST) & 1, p.err, abort_flag))) break;
+        tc_fence_after();
+        for (int w = 0; w < 2; ++w) issue_S(w, g);
+        tc_commit(&bar->k_empty[g % NST]);
+        bool first = true;
+        while (ok) {
+          const int st = g % NST;
+          const bool last = *const_cast<volatile int*>(&bar->desc[g & 3].last) != 0;
+          for (int w = 0; w < 2; ++w) {
+            if (!(ok = mbar_wait(&bar->p_ready[w], g & 1, p.err, abort_flag))) break;
+            if (w == 0 && !(ok = mbar_wait(&bar->v_full[st], (g / NST) & 1, p.err, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t aP = tmem + C::COL_S + w * 128 + C::COL_P;
+            const uint32_t vlo = sdesc_lo(sVa + st * C::TILE, C::BOX);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tmem + C::COL_O + w * D, aP + kk * 8, sdesc_join(vlo + kk * (2048 >> 4), kDescHi), idO,
+                     (!first || kk > 0) ? 1u : 0u);
+            tc_commit(&bar->pv_done[w]);
+            if (w == 1) tc_commit(&bar->v_empty[st]);
+            if (!last) {
+              const int gn = g + 1;
+              if (w == 0) {
+                if (!(ok = mbar_wait(&bar->k_full[gn % NST], (gn / NST) & 1, p.err, abort_flag))) break;
+                tc_fence_after();
+              }
+              issue_S(w, gn);
+              if (w == 1) tc_commit(&bar->k_empty[gn % NST]);
+            }
+          }
+          first = false;
+          ++g;
+          if (last) break;
+        }
+      }
+      tc_commit(&bar->drain);
+      mbar_wait(&bar->drain, 0, nullptr, nullptr);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax, one row per thread
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::COL_S + w * 128, tP = tS + C::COL_P, tO = tmem + lane_off + C::COL_O + w * D;
+    bool ok = true;
+    int g = 0, slot = 0;
+    for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
+      const Item it = chunk_item(p, base, x);
+      const int r = it.r0 + w * 128 + row;
+      const bool live = r < it.rows;
+      const int tok = live ? r / p.G : 0, hq = it.h * p.G + (live ? r - tok * p.G : 0);
+      const int pos = live ? it.q.lead + tok : -1;
+      {
+        // ---- the row of Q as fp16, its largest magnitude in [2^13, 2^14)
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (long long)(it.q.tok0 + tok) * p.q_tok + (long long)hq * p.q_head;
+        float top = 0.f;
+        auto pair = [&](uint32_t v) {
+          return p.bf16 ? make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u))
+                        : __half22float2(*reinterpret_cast<const __half2*>(&v));
+        };
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = pair(vs[y]);
+            if (fabsf(f.x) <= 3.402823466e38f) top = fmaxf(top, fabsf(f.x));
+            if (fabsf(f.y) <= 3.402823466e38f) top = fmaxf(top, fabsf(f.y));
+          }
+        }
+        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+        const int sh = max(-110, min(110, 13 - ex));
+        const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = pair(vs[y]);
+            o[y] = pack_half2(f.x * up, f.y * up);
+          }
+          *reinterpret_cast<uint4*>(sQ + w * C::TILE + (c >> 3) * C::BOX + sw128_offset(row, c & 7)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bar->q_full[w]);
+        const float down = __uint_as_float((uint32_t)(127 - sh) << 23);
+        float sc = 0.f, m_run = -INFINITY, l_run = 0.f;
+        bool first = true;
+        for (;;) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar->s_full[w], g & 1, p.err, abort_flag)))) break;
+          tc_fence_after();
+          const volatile TileDesc* ds = &bar->desc[g & 3];
+          if (first) {  // never 0, so that a masked score stays -inf (keys that all are 0: any factor)
+            const int ek = bar->ex_k[slot];
+            sc = fmaxf(p.scale_log2 * down * (ek ? __uint_as_float((uint32_t)ek << 23) : 1.f), 1.17549435e-38f);
+          }
+          const int k0 = ds->k0;
+          const bool last = ds->last != 0;
+          uint32_t keep[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) keep[y] = ds->valid[y];
+          bool full = (keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu;
+          if (k0 >= 0) {
+            full = full && k0 + 127 <= pos && pos - k0 < p.n;
+            if (!full) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) keep[y] &= window_keep_word(y, pos, k0, p.n, kMaxLen, ds->anchor[y]);
+            }
+          } else if (pos < 0) {
+            full = false;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) keep[y] = 0;
+          }
+          const bool mask = __any_sync(0xffffffffu, !full);
+          // ---- row maximum
+          uint32_t s[64];
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto load_half = [&](int hf) {
+            tmem_ld32(tS + hf * 64, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tS + hf * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_ld_wait();
+            if (mask) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (!((keep[hf * 2 + (c >> 5)] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+            }
+          };
+          auto max_half = [&]() {
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              mx4[(c >> 1) & 3] = fmax3(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          };
+          load_half(0);
+          max_half();
+          load_half(1);
+          max_half();
+          const float m_tile = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
+          float alpha = 1.0f;
+          bool rescale = false;
+          if (first) {
+            m_run = m_tile;
+          } else {
+            const bool need = m_tile > m_run + 8.0f;
+            rescale = __any_sync(0xffffffffu, need);
+            if (need) {
+              alpha = ex2(m_run - m_tile);
+              l_run *= alpha;
+              m_run = m_tile;
+            }
+          }
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          // ---- P: keys 64.. from registers, then keys 0..63 loaded again (P lies over S's upper half)
+          float2 sum4[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sum4[y] = make_float2(0.f, 0.f);
+          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
+          auto weigh = [&]() {
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float2 v = f2_fma(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, nm2);
+              const float2 e = make_float2(ex2(v.x), ex2(v.y));
+              sum4[(c >> 1) & 3] = f2_add(sum4[(c >> 1) & 3], e);
+              s[c >> 1] = pack_half2(e.x, e.y);
+            }
+          };
+          weigh();
+          tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+          load_half(0);
+          weigh();
+          tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+          l_run += ((sum4[0].x + sum4[0].y) + (sum4[1].x + sum4[1].y)) + ((sum4[2].x + sum4[2].y) + (sum4[3].x + sum4[3].y));
+          if (rescale) {  // this tile's S was issued behind the last P V, which is therefore complete
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t ov[32];
+              tmem_ld32(tO + cc * 32, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * alpha);
+              tmem_st32(tO + cc * 32, ov);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bar->p_ready[w]);
+          first = false;
+          ++g;
+          if (last) break;
+        }
+        if (!ok) break;
+        // ---- output
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar->pv_done[w], (g - 1) & 1, p.err, abort_flag)))) break;
+        tc_fence_after();
+        const bool none = m_run == -INFINITY && !(l_run != l_run);
+        const float f = none ? 0.f : __uint_as_float((uint32_t)bar->ex_v[slot] << 23) / l_run;
+        const long long orow = ((long long)(it.q.tok0 + tok) * p.Hq + hq) * D;
+        uint16_t* out = static_cast<uint16_t*>(p.o) + orow;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t ov[32];
+          tmem_ld32(tO + cc * 32, ov);
+          tmem_ld_wait();
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float a = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z]) * f;
+                const float b = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z + 1]) * f;
+                pk[z] = p.bf16 ? pack_bf16x2(a, b) : pack_half2(a, b);
+              }
+              *reinterpret_cast<uint4*>(out + cc * 32 + 8 * y) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+        }
+        if (live && p.lse)
+          p.lse[(long long)(it.q.tok0 + tok) * p.Hq + hq] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+        // ---- NaN among the values, rare: the row looks for the keys it keeps that have one
+        if (live && *const_cast<volatile int*>(&bar->nan[slot])) {
+          const int32_t* table = p.table + (long long)it.seq * p.max_pages;
+          for (int j = 0; j <= pos; ++j) {
+            const int id = __ldg(table + (j >> p.log_page));
+            if (id < 0 || id >= p.num_pages) continue;
+            const int off = j & ((1 << p.log_page) - 1);
+            if (!(pos - j < p.n || j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + off) != 0)) continue;
+            const uint8_t* v = p.v_pages + ((((size_t)id * p.Hkv + it.h) << p.log_page) + off) * D;
+            for (int c = 0; c < D / 4; ++c) {
+              const uint32_t b = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(v) + c));
+              for (int y = 0; y < 4; ++y)
+                if (b >> (8 * y) & 0x80u) out[4 * c + y] = 0x7fffu;  // NaN in bf16 and fp16
+            }
+          }
+        }
+        tc_fence_before();
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_chunks_t(const PagedAttnParams& p, cudaStream_t stream) {
+  const size_t smem = chunk_smem_bytes<D>(p.S);
+  static_assert(chunk_smem_bytes<128>(4096) <= 227 * 1024, "shared memory budget");
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !set[dev].load()) {
+    e = cudaFuncSetAttribute(paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)chunk_smem_bytes<D>(4096));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev].store(true);
+  }
+  return launch_chained(paged_chunk_kernel<D>, dim3(148), dim3(ChunkCfg<D>::THREADS), smem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunks(const PagedAttnParams& p, int d, cudaStream_t stream) {
+  return d == 128 ? launch_chunks_t<128>(p, stream) : launch_chunks_t<64>(p, stream);
+}
+
+}  // namespace sep

@@ -822,6 +822,8 @@ class SepPagedCache:
         n = INT32_MAX if n is None else int(n)
         if not 0 <= a <= INT32_MAX or not 0 <= n <= INT32_MAX:
             raise SepError(f"a = {a} and n = {n} must be between 0 and 2^31 - 1")
+        if scale is not None and not 0.0 < scale < math.inf:
+            raise SepError(f"scale = {scale} must be positive")
         scale = self.d ** -0.5 if scale is None else scale
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)

@@ -140,16 +140,20 @@ def paged_attend(q, k, v, flag, a, n, scale):
     c, Hq, d = q.shape
     length, G = k.shape[0], q.shape[1] // k.shape[1]
     o, mag, lse = np.zeros((c, Hq, d)), np.zeros((c, Hq, d)), np.full((c, Hq), -math.inf)
+    j = np.arange(length)
+    anchor = (j < a) | np.asarray(flag, dtype=bool)
     for i in range(c):
         p = length - c + i
-        keep = np.array([j for j in range(length) if j <= p and (p - j < n or j < a or flag[j])], dtype=int)
+        keep = np.nonzero((j <= p) & ((p - j < n) | anchor))[0]
         if keep.size == 0:
             continue
-        for hq in range(Hq):
-            s = scale * (k[keep, hq // G] @ q[i, hq])
-            top = s.max()
+        for h in range(k.shape[1]):
+            hs = slice(h * G, h * G + G)
+            s = scale * (q[i, hs] @ k[keep, h].T)
+            top = s.max(1, keepdims=True)
             w = np.exp(s - top)
-            o[i, hq] = (w / w.sum()) @ v[keep, hq // G]
-            mag[i, hq] = (w / w.sum()) @ np.abs(v[keep, hq // G])
-            lse[i, hq] = top + math.log(w.sum())
+            total = w.sum(1, keepdims=True)
+            o[i, hs] = (w / total) @ v[keep, h]
+            mag[i, hs] = (w / total) @ np.abs(v[keep, h])
+            lse[i, hs] = (top + np.log(total))[:, 0]
     return o, lse, mag

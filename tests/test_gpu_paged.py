@@ -227,16 +227,17 @@ def filled(S, seqs, lens, Hkv, d, page, seed, p=0.2, spread=2, extra_pages=0):
 
 
 def sequence(pair, s, length):
-    """Stored values, flags and the largest value scale of one sequence."""
+    """Stored values, flags and the value scales of one sequence."""
+    import torch
     page = pair.cache.page
-    ids = pair.table[s][np.arange(length) // page]
-    sl = np.arange(length) % page
+    ids = torch.from_numpy(pair.table[s][np.arange(length) // page]).cuda()
+    sl = torch.from_numpy(np.arange(length) % page).cuda()
     out = []
     for x in "kv":
-        num = P.e4m3_decode(codes(getattr(pair.cache, x + "_pages")))[ids, :, sl]
-        out.append(num * getattr(pair.cache, x + "_scale").double().cpu().numpy()[ids][:, :, None])
-    vs = pair.cache.v_scale.double().cpu().numpy()[ids]
-    return out[0], out[1], pair.cache.flags.cpu().numpy()[ids, sl] != 0, vs
+        num = P.e4m3_decode(getattr(pair.cache, x + "_pages").view(torch.uint8)[ids, :, sl].cpu().numpy())
+        out.append(num * getattr(pair.cache, x + "_scale")[ids].double().cpu().numpy()[:, :, None])
+    vs = pair.cache.v_scale[ids].double().cpu().numpy()
+    return out[0], out[1], pair.cache.flags[ids, sl].cpu().numpy() != 0, vs
 
 
 def check_attn(pair, q, o, lse, counts, a, n, scale, only=None):
@@ -254,7 +255,7 @@ def check_attn(pair, q, o, lse, counts, a, n, scale, only=None):
         k, v, flag, vs = sequence(pair, s, L)
         ro, rl, mag = P.paged_attend(qn[r], k, v, flag, a, n if n is not None else 1 << 40, scale)
         G = qn.shape[1] // k.shape[1]
-        dot = np.einsum("ihd,jhd->ihj", np.abs(qn[r]), np.abs(np.repeat(k, G, 1))) if L else np.zeros((c, 1, 1))
+        dot = np.einsum("ihd,jhd->ihj", np.abs(qn[r]), np.abs(np.repeat(k, G, 1))) if L else np.zeros((c, qn.shape[1], 1))
         ds = 2.0 ** -19 * scale * dot.max(-1, initial=0.0)
         # max(p vs) <= the largest scale
         floor = L * 2.0 ** -25 * 448.0 * (np.repeat(vs, G, 1).max(0, initial=0.0) if L else 0.0)
@@ -265,7 +266,7 @@ def check_attn(pair, q, o, lse, counts, a, n, scale, only=None):
         dead = np.isneginf(rl)
         assert np.array_equal(np.isneginf(ln[r]), dead) and np.all(on[r][dead] == 0.0)
         live = ~dead
-        assert np.all(np.abs(ln[r] - rl)[live] <= (2 * ds + 2.0 ** -20 * (1 + np.abs(rl)))[live])
+        assert np.all(np.abs(ln[r][live] - rl[live]) <= 2 * ds[live] + 2.0 ** -20 * (1 + np.abs(rl[live])))
 
 
 ATTN = [
@@ -281,6 +282,15 @@ ATTN = [
     ((300, 800), (4, 2), 24, 1, 64, 64, "bfloat16", 3, 1),      # more heads in a group than a tile has rows
     ((620, 2100), (3, 1), 4, 2, 128, 64, "bfloat16", 5, 0),     # no window: initial tokens and separators
     ((3, 1), (5, 4), 4, 2, 64, 16, "bfloat16", 0, None),        # queries before position 0
+    # chunks (more than 32 (token, head) rows): one and several row tiles, decode rows beside them
+    ((40,), (40,), 1, 1, 64, 16, "float16", 0, None),
+    ((700,), (257,), 1, 1, 128, 64, "bfloat16", 0, None),
+    ((513, 90, 1300), (200, 1, 65), 8, 2, 128, 128, "bfloat16", 0, None),
+    ((1500, 300), (130, 33), 6, 2, 64, 32, "float16", 3, 100),
+    ((2600,), (90,), 14, 2, 128, 16, "bfloat16", 4, 256),
+    ((400,), (300,), 2, 1, 64, 64, "bfloat16", 2, 0),            # no window
+    ((1400, 50, 0, 7), (100, 80, 60, 50), 3, 3, 64, 16, "bfloat16", 1, 1),  # queries before position 0, no key
+    ((300,) * 9, (40,) * 9, 16, 16, 64, 64, "float16", 0, None),  # more items than SMs
 ]
 
 
@@ -356,16 +366,17 @@ def test_page_scales_far_apart(S):
 
 
 @pytest.mark.parametrize("what", ["key", "value"])
-def test_nan_reaches_only_the_rows_that_keep_it(S, what):
+@pytest.mark.parametrize("c", [12, 40])  # few rows, a chunk
+def test_nan_reaches_only_the_rows_that_keep_it(S, what, c):
     """A NaN in one token: queries that keep the token see it, the others (earlier, or out of their
     window) do not, and neither do numbers in slots behind the sequence."""
     import torch
-    L, c, n = 150, 12, 20
+    L, n = 150, 20
     pair = filled(S, 1, (L,), 2, 64, 16, seed=9, p=0.0)
     q = draw(4, c, 4, 64, torch.bfloat16)
     plan = (ints(pair.table.tolist()), ints([L]), ints([0, c]))
     clean, clean_lse = pair.cache.seppaged_attn(q, *plan, n=n)
-    j = L - 7                      # tokens L - 12 .. L - 8 do not see it
+    j = L - 7                      # earlier tokens do not see it
     pages = getattr(pair.cache, ("k" if what == "key" else "v") + "_pages").view(torch.uint8)
     pages[int(pair.table[0][j // 16]), 1, j % 16, 5] = 0xFF
     jj = L - c - n + 3             # leaves the window of the later queries
@@ -384,6 +395,46 @@ def test_nan_reaches_only_the_rows_that_keep_it(S, what):
             else:
                 assert torch.isnan(o[i, hq, t[1]]) and torch.isnan(o[i, hq]).sum() == 1
                 assert torch.equal(lse[i, hq], clean_lse[i, hq])
+
+
+def test_chunk_with_pages_of_zeros_and_far_scales(S):
+    """A chunk over pages whose scales differ: within 2^15 of the largest nothing changes, below that the
+    numbers are rounded to 2^-25 of the largest scale (2^-33 of the largest magnitude); pages of zeros."""
+    import torch
+    pair = Pair(S, 1, 8, 2, 64, 16)
+    k, v = draw(1, 128, 2, 64, torch.bfloat16, 0), draw(2, 128, 2, 64, torch.bfloat16, 0)
+    k[16:32] *= 2.0 ** -14
+    v[16:32] *= 2.0 ** 12
+    v[32:48] = 0.0
+    k[48:64] = 0.0
+    v[64:80] *= 2.0 ** -40
+    pair.append(k, v, None, (128,))
+    q = draw(3, 60, 4, 64, torch.bfloat16, 1)
+    o, lse = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints([128]), ints([0, 60]))
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    check_attn(pair, q, o, lse, (60,), 0, None, 0.125)
+    # all keys, then all values zero: uniform weights, zero outputs
+    pair.cache.k_pages.view(torch.uint8).zero_()
+    pair.cache.k_scale.zero_()
+    o, lse = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints([128]), ints([0, 60]))
+    check_attn(pair, q, o, lse, (60,), 0, None, 0.125)
+    pair.cache.v_pages.view(torch.uint8).zero_()
+    pair.cache.v_scale.zero_()
+    o, lse = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints([128]), ints([0, 60]))
+    assert (o == 0).all() and torch.allclose(lse, torch.log(torch.arange(69., 129., device="cuda"))[:, None], atol=1e-5)
+
+
+def test_chunk_of_every_anchor_density(S):
+    """Lists of kept keys that end inside a tile, at its end, and fill several refills."""
+    import torch
+    for p, a in ((0.0, 0), (0.0, 128), (0.02, 5), (1.0, 0)):
+        pair = filled(S, 1, (2500,), 1, 64, 64, seed=int(100 * p) + a, p=p)
+        q = draw(9, 45, 2, 64, torch.bfloat16)
+        o, lse = pair.cache.seppaged_attn(q, ints(pair.table.tolist()), ints([2500]), ints([0, 45]), a=a, n=33)
+        torch.cuda.synchronize()
+        assert S.sep_last_device_error() == 0
+        check_attn(pair, q, o, lse, (45,), a, 33, 0.125)
 
 
 def test_long_sequence(S):
