@@ -39,6 +39,9 @@ constexpr int kScanStep = 1024;  // positions examined per refill of the list
 struct __align__(8) KeyRow {
   uint32_t row, ex;  // pool row (kNoRow: none), exponent fields of its page's scales
 };
+struct __align__(8) KeyPut {
+  uint32_t row, f;  // pool row, fp16 factors of its key (low) and value numbers
+};
 
 template <int D>
 struct ChunkCfg {
@@ -62,12 +65,13 @@ struct ChunkBar {
   uint64_t q_full[2], s_full[2], p_ready[2], pv_done[2];
   uint64_t conv, drain;
   TileDesc desc[4];
-  KeyRow keys[2][128];
+  KeyPut keys[2][128];
+  uint32_t far[2][128];  // second factors, 1.0 each unless a page lies 2^-24 below the largest
   // By item modulo 4 (an item's first tile waits for the products of three tiles before, so its slot has
   // been read by then): exponent fields of the largest scales, a NaN among the values.
   int ex_k[4], ex_v[4], nan[4];
-  int red[4], part4[4];
-  long long part[13];
+  int red[4], part4[4], any_far[2][4];
+  int part[16];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -111,48 +115,65 @@ __device__ __forceinline__ Item chunk_item(const PagedAttnParams& p, const int* 
   return it;
 }
 
+// mbar_wait with long waits left to the hardware: the tries suspend the warp for up to kSuspendNs, so that
+// waiting roles take no issue slots from the working ones (2048 queries over 8192 keys: 478 us without).
+constexpr uint32_t kSuspendNs = 20000;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort_flag) {
+  const uint32_t a = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      record_failure(err, abort_flag, SEP_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// Largest of three, NaN if one is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4)  // D f32; A and B f16 (format 0)
          | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Four e4m3 numbers as fp16 times f * f2 (powers of two).
-__device__ __forceinline__ uint2 widen4(uint32_t w, __half2 f, __half2 f2, bool far) {
-  uint32_t lo = cvt_e4m3x2(w), hi = cvt_e4m3x2_hi(w);
-  __half2 a = __hmul2(*reinterpret_cast<__half2*>(&lo), f), b = __hmul2(*reinterpret_cast<__half2*>(&hi), f);
-  if (far) {
-    a = __hmul2(a, f2);
-    b = __hmul2(b, f2);
-  }
-  return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+// 2^e as fp16 bits, e in [-24, 0]
+__device__ __forceinline__ uint32_t half_pow2(int e) { return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24); }
+// Power of two from a page's scale to the largest one (exponent fields), in two factors. Beyond 2^-48 every
+// number rounds to 0; a page of zeros may take any factor.
+__device__ __forceinline__ void shift_of(int ex, int top, uint32_t* f, uint32_t* f2) {
+  const int e = ex == 0 ? 0 : max(ex - top, -48);
+  *f = half_pow2(max(e, -24));
+  *f2 = half_pow2(max(min(e + 24, 0), -24));
 }
-// 2^e as fp16, e in [-24, 0]
-__device__ __forceinline__ __half2 half_pow2(int e) {
-  const uint16_t b = e >= -14 ? (uint16_t)((e + 15) << 10) : (uint16_t)(1u << (e + 24));
-  const __half h = *reinterpret_cast<const __half*>(&b);
-  return __half2half2(h);
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t f) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&f));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
-// Factors of a page whose scale has exponent field ex against the largest's, top. Beyond 2^-48 every
-// number rounds to 0.
-struct Shift {
-  __half2 f, f2;
-  bool far;
-};
-__device__ __forceinline__ Shift shift_of(int ex, int top) {
-  const int e = ex == 0 ? 0 : max(ex - top, -48);  // a page of zeros: any factor
-  Shift s;
-  s.far = e < -24;
-  s.f = half_pow2(max(e, -24));
-  s.f2 = half_pow2(max(min(e + 24, 0), -24));
-  return s;
-}
+constexpr uint32_t kOnes = 0x3c003c00u;
 
 template <int D>
 __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(const __grid_constant__ PagedAttnParams p) {
   using C = ChunkCfg<D>;
   constexpr int NST = C::NST;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: the compiler keeps shared-memory instructions)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;  // two row tiles
   uint8_t* sK = sQ + 2 * C::TILE;
   uint8_t* sV = sK + NST * C::TILE;
@@ -196,8 +217,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     __syncthreads();
     int before = carry;
     for (int w = 0; w < C::THREADS / 32; ++w) {
-      if (w < warp) before += (int)bar->part[w];
-      carry += (int)bar->part[w];
+      if (w < warp) before += bar->part[w];
+      carry += bar->part[w];
     }
     if (s < p.S) base[s] = before + inc - x;
     __syncthreads();
@@ -223,7 +244,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     // barrier of the 128 converter threads, bounded like every other wait
     auto conv_sync = [&]() -> bool {
       mbar_arrive(&bar->conv);
-      const bool r = __all_sync(0xffffffffu, mbar_wait(&bar->conv, syncs & 1, p.err, abort_flag));
+      const bool r = __all_sync(0xffffffffu, wait_bar(&bar->conv, syncs & 1, p.err, abort_flag));
       ++syncs;
       return r;
     };
@@ -261,12 +282,19 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
       // ---- the tiles: listed keys, then the window
       int list_at = 0, list_n = 0, scan = 0, win = it.w0;
       bool any = false;
-      KeyRow e;        // this thread's key of the next tile
-      int e_k0;        // its window position, -1 listed, -2 no further tile
-      bool e_anchor;
+      // This thread's key of the next tile. Its scales and flag are requested by next_tile and looked at a
+      // tile later; its page number is requested a tile earlier still.
+      uint32_t e_row = kNoRow, e_ex = 0;
+      float e_ks = 0.f, e_vs = 0.f;
+      int e_k0 = -2;  // its window position, -1 listed, -2 no further tile
+      int e_flag = 0;
+      int id_next = -1;  // page of position win + t
+      if (win + t < it.kend) id_next = __ldg(table + ((win + t) >> p.log_page));
       auto next_tile = [&]() -> bool {
-        e = KeyRow{kNoRow, 0};
-        e_anchor = false;
+        e_row = kNoRow;
+        e_ks = e_vs = 0.f;
+        e_ex = 0;
+        e_flag = 0;
         while (list_n - list_at < 128 && scan < it.w0) {
           // what is left moves to the front, then kScanStep more positions are examined, 8 per thread
           const int rem = list_n - list_at;
@@ -317,7 +345,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           if (!conv_sync()) return false;
         }
         if (list_at < list_n) {
-          if (list_at + t < list_n) e = list[list_at + t];
+          if (list_at + t < list_n) {
+            const KeyRow e = list[list_at + t];
+            e_row = e.row;
+            e_ex = e.ex;
+          }
           list_at = min(list_at + 128, list_n);
           e_k0 = -1;
           any = true;
@@ -328,18 +360,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           return true;
         }
         const int j = win + t;
-        if (j < it.kend) {
-          const int id = __ldg(table + (j >> p.log_page));
-          if (id >= 0 && id < p.num_pages) {
-            const size_t sc = (size_t)id * p.Hkv + it.h;
-            const int off = j & ((1 << p.log_page) - 1);
-            e.row = (uint32_t)(sc << p.log_page) + off;
-            e.ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
-            // flags matter where the last row's window does not reach
-            if (it.kend - 1 - win >= p.n)
-              e_anchor = j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + off) != 0;
-          }
+        if (j < it.kend && id_next >= 0 && id_next < p.num_pages) {
+          const size_t sc = (size_t)id_next * p.Hkv + it.h;
+          const int off = j & ((1 << p.log_page) - 1);
+          e_row = (uint32_t)(sc << p.log_page) + off;
+          e_ks = __ldg(p.k_scale + sc);
+          e_vs = __ldg(p.v_scale + sc);
+          // flags matter where the last row's window does not reach
+          if (it.kend - 1 - win >= p.n)
+            e_flag = j < p.a ? 1 : (int)__ldg(p.flags + ((size_t)id_next << p.log_page) + off);
         }
+        id_next = j + 128 < it.kend ? __ldg(table + ((j + 128) >> p.log_page)) : -1;
         e_k0 = win;
         win += 128;
         any = true;
@@ -349,20 +380,30 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
       for (;;) {
         const int st = g % NST, rnd = g / NST;
         const int k0 = e_k0;
-        const uint32_t vmask = __ballot_sync(0xffffffffu, e.row != kNoRow);
-        const uint32_t amask = __ballot_sync(0xffffffffu, e_anchor);
-        bar->keys[g & 1][t] = e;
+        const uint32_t vmask = __ballot_sync(0xffffffffu, e_row != kNoRow);
+        const uint32_t amask = __ballot_sync(0xffffffffu, e_flag != 0);
+        {
+          const uint32_t exs = k0 < 0 ? e_ex : scale_exponents(e_ks, e_vs);
+          uint32_t fk, fk2, fv, fv2;
+          shift_of(exs & 0xffu, ek, &fk, &fk2);
+          shift_of(exs >> 8, ev, &fv, &fv2);
+          bar->keys[g & 1][t] = KeyPut{e_row, fk | fv << 16};
+          bar->far[g & 1][t] = fk2 | fv2 << 16;
+          const bool w_far = __any_sync(0xffffffffu, (fk2 | fv2 << 16) != kOnes);
+          if (lane == 0) bar->any_far[g & 1][cw] = w_far;
+        }
         if (!(ok = conv_sync())) break;
-        // ---- this thread's pieces of the tile's rows: 16 numbers of one row at a time
+        // ---- this thread's pieces of the tile's rows: 16 numbers of one row at a time, rows of its warp
         constexpr int PPR = D / 16, RPI = 32 / PPR, NI = 32 / RPI;  // pieces per row, rows per load, loads
         const int piece = lane % PPR;
+        const bool far = bar->any_far[g & 1][cw] != 0;
         uint4 kx[NI], vx[NI];
-        uint32_t ex[NI];
+        uint32_t fx[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const KeyRow kr = bar->keys[g & 1][cw * 32 + i * RPI + lane / PPR];
+          const KeyPut kr = bar->keys[g & 1][cw * 32 + i * RPI + lane / PPR];
           kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
-          ex[i] = kr.ex;
+          fx[i] = kr.f;
           if (kr.row != kNoRow) {
             kx[i] = __ldg(reinterpret_cast<const uint4*>(p.k_pages + (size_t)kr.row * D + piece * 16));
             vx[i] = __ldg(reinterpret_cast<const uint4*>(p.v_pages + (size_t)kr.row * D + piece * 16));
@@ -370,7 +411,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         }
         if (!(ok = next_tile())) break;  // its loads go out behind the rows'
         const bool last = e_k0 == -2;
-        if (rnd > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bar->k_empty[st], (rnd - 1) & 1, p.err, abort_flag)))) break;
+        if (rnd > 0 && !(ok = __all_sync(0xffffffffu, wait_bar(&bar->k_empty[st], (rnd - 1) & 1, p.err, abort_flag)))) break;
         TileDesc* ds = &bar->desc[g & 3];
         if (lane == 0) {
           ds->valid[cw] = vmask;
@@ -380,48 +421,69 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           ds->k0 = k0;
           ds->last = last;
         }
-        auto put = [&](uint8_t* tile, int i, uint4 v, Shift sh) {
+        auto put = [&](uint8_t* tile, int i, const uint4& v, uint32_t sel, bool far) {
           const int r = cw * 32 + i * RPI + lane / PPR;
-          const uint2 a = widen4(v.x, sh.f, sh.f2, sh.far), b = widen4(v.y, sh.f, sh.f2, sh.far);
-          const uint2 c = widen4(v.z, sh.f, sh.f2, sh.far), d = widen4(v.w, sh.f, sh.f2, sh.far);
+          const uint32_t f = __byte_perm(fx[i], 0, sel);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            h[2 * y] = hmul2(cvt_e4m3x2(w[y]), f);
+            h[2 * y + 1] = hmul2(cvt_e4m3x2_hi(w[y]), f);
+          }
+          if (far) {
+            const uint32_t f2 = __byte_perm(bar->far[g & 1][r], 0, sel);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) h[y] = hmul2(h[y], f2);
+          }
           // elements 16 piece ..: box piece / 4, chunks 2 (piece % 4) and the next; lanes of the second box
           // store theirs in the other order, so that eight lanes touch every bank once
-          uint8_t* box = tile + (piece >> 2) * C::BOX;
-          const int ch = 2 * (piece & 3);
-          const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-          const bool swap = piece & 4;
-          *reinterpret_cast<uint4*>(box + sw128_offset(r, ch + (swap ? 1 : 0))) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(box + sw128_offset(r, ch + (swap ? 0 : 1))) = swap ? lo : hi;
+          uint8_t* row = tile + (piece >> 2) * C::BOX + r * 128;
+          const int c0 = (2 * (piece & 3)) ^ (r & 7), second = piece >> 2 & 1;
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(row + ((c0 ^ second) << 4)) = second ? hi : lo;
+          *reinterpret_cast<uint4*>(row + ((c0 ^ second ^ 1) << 4)) = second ? lo : hi;
         };
+        if (!far) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) put(sK + st * C::TILE, i, kx[i], shift_of(ex[i] & 0xff, ek));
+          for (int i = 0; i < NI; ++i) put(sK + st * C::TILE, i, kx[i], 0x1010, false);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) put(sK + st * C::TILE, i, kx[i], 0x1010, true);
+        }
         fence_proxy_async_smem();
         mbar_arrive(&bar->k_full[st]);
         uint32_t bad = 0;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const uint32_t n0 = nan_bytes(vx[i].x), n1 = nan_bytes(vx[i].y), n2 = nan_bytes(vx[i].z), n3 = nan_bytes(vx[i].w);
-          if (n0 | n1 | n2 | n3) {
-            bad = 1;
-            vx[i].x &= ~((n0 >> 7) * 0xffu);
-            vx[i].y &= ~((n1 >> 7) * 0xffu);
-            vx[i].z &= ~((n2 >> 7) * 0xffu);
-            vx[i].w &= ~((n3 >> 7) * 0xffu);
-          }
-        }
-        if (bad) *const_cast<volatile int*>(&bar->nan[slot]) = 1;
-        if (rnd > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bar->v_empty[st], (rnd - 1) & 1, p.err, abort_flag)))) break;
+        for (int i = 0; i < NI; ++i)
+          bad |= nan_bytes(vx[i].x) | nan_bytes(vx[i].y) | nan_bytes(vx[i].z) | nan_bytes(vx[i].w);
+        if (bad) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) put(sV + st * C::TILE, i, vx[i], shift_of(ex[i] >> 8, ev));
+          for (int i = 0; i < NI; ++i) {
+            vx[i].x &= ~((nan_bytes(vx[i].x) >> 7) * 0xffu);
+            vx[i].y &= ~((nan_bytes(vx[i].y) >> 7) * 0xffu);
+            vx[i].z &= ~((nan_bytes(vx[i].z) >> 7) * 0xffu);
+            vx[i].w &= ~((nan_bytes(vx[i].w) >> 7) * 0xffu);
+          }
+          bar->nan[slot] = 1;
+        }
+        if (rnd > 0 && !(ok = __all_sync(0xffffffffu, wait_bar(&bar->v_empty[st], (rnd - 1) & 1, p.err, abort_flag)))) break;
+        if (!far) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) put(sV + st * C::TILE, i, vx[i], 0x3232, false);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) put(sV + st * C::TILE, i, vx[i], 0x3232, true);
+        }
         fence_proxy_async_smem();
         mbar_arrive(&bar->v_full[st]);
         ++g;
         if (last) break;
       }
     }
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
+    if (warp == 12 && lane == 0) {
       constexpr uint32_t idS = make_idesc_f16(128, 128, false), idO = make_idesc_f16(128, D, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
       bool ok = true;
@@ -437,19 +499,19 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         tc_commit(&bar->s_full[w]);
       };
       for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, ++item) {
-        if (!(ok = mbar_wait(&bar->q_full[0], item & 1, p.err, abort_flag))) break;
-        if (!(ok = mbar_wait(&bar->q_full[1], item & 1, p.err, abort_flag))) break;
-        if (!(ok = mbar_wait(&bar->k_full[g % NST], (g / NST) & 1, p.err, abort_flag))) break;
+        if (!(ok = wait_bar(&bar->q_full[0], item & 1, p.err, abort_flag))) break;
+        if (!(ok = wait_bar(&bar->q_full[1], item & 1, p.err, abort_flag))) break;
+        if (!(ok = wait_bar(&bar->k_full[g % NST], (g / NST) & 1, p.err, abort_flag))) break;
         tc_fence_after();
         for (int w = 0; w < 2; ++w) issue_S(w, g);
         tc_commit(&bar->k_empty[g % NST]);
         bool first = true;
         while (ok) {
           const int st = g % NST;
-          const bool last = *const_cast<volatile int*>(&bar->desc[g & 3].last) != 0;
+          const bool last = bar->desc[g & 3].last != 0;
           for (int w = 0; w < 2; ++w) {
-            if (!(ok = mbar_wait(&bar->p_ready[w], g & 1, p.err, abort_flag))) break;
-            if (w == 0 && !(ok = mbar_wait(&bar->v_full[st], (g / NST) & 1, p.err, abort_flag))) break;
+            if (!(ok = wait_bar(&bar->p_ready[w], g & 1, p.err, abort_flag))) break;
+            if (w == 0 && !(ok = wait_bar(&bar->v_full[st], (g / NST) & 1, p.err, abort_flag))) break;
             tc_fence_after();
             const uint32_t aP = tmem + C::COL_S + w * 128 + C::COL_P;
             const uint32_t vlo = sdesc_lo(sVa + st * C::TILE, C::BOX);
@@ -462,7 +524,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
             if (!last) {
               const int gn = g + 1;
               if (w == 0) {
-                if (!(ok = mbar_wait(&bar->k_full[gn % NST], (gn / NST) & 1, p.err, abort_flag))) break;
+                if (!(ok = wait_bar(&bar->k_full[gn % NST], (gn / NST) & 1, p.err, abort_flag))) break;
                 tc_fence_after();
               }
               issue_S(w, gn);
@@ -529,11 +591,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         mbar_arrive(&bar->q_full[w]);
         const float down = __uint_as_float((uint32_t)(127 - sh) << 23);
         float sc = 0.f, m_run = -INFINITY, l_run = 0.f;
-        bool first = true;
+        bool first = true, row_nan = false;
         for (;;) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar->s_full[w], g & 1, p.err, abort_flag)))) break;
+          if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->s_full[w], g & 1, p.err, abort_flag)))) break;
           tc_fence_after();
-          const volatile TileDesc* ds = &bar->desc[g & 3];
+          const TileDesc* ds = &bar->desc[g & 3];
           if (first) {  // never 0, so that a masked score stays -inf (keys that all are 0: any factor)
             const int ek = bar->ex_k[slot];
             sc = fmaxf(p.scale_log2 * down * (ek ? __uint_as_float((uint32_t)ek << 23) : 1.f), 1.17549435e-38f);
@@ -556,29 +618,42 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
             for (int y = 0; y < 4; ++y) keep[y] = 0;
           }
           const bool mask = __any_sync(0xffffffffu, !full);
+          // ---- masked scores become -inf in place (few tiles: the loops below stay short, they have to
+          // fit the instruction cache beside the other roles)
+          if (mask) {
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y) {
+              uint32_t s[32];
+              tmem_ld32(tS + y * 32, s);
+              tmem_ld_wait();
+              const uint32_t kw = y == 0 ? keep[0] : y == 1 ? keep[1] : y == 2 ? keep[2] : keep[3];
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((kw >> c) & 1u)) s[c] = 0xff800000u;
+              tmem_st32(tS + y * 32, s);
+            }
+            tmem_st_wait();
+          }
           // ---- row maximum
           uint32_t s[64];
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           auto load_half = [&](int hf) {
             tmem_ld32(tS + hf * 64, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
             tmem_ld32(tS + hf * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tmem_ld_wait();
-            if (mask) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (!((keep[hf * 2 + (c >> 5)] >> (c & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
-            }
           };
-          auto max_half = [&]() {
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            load_half(hf);
 #pragma unroll
             for (int c = 0; c < 64; c += 2)
-              mx4[(c >> 1) & 3] = fmax3(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          };
-          load_half(0);
-          max_half();
-          load_half(1);
-          max_half();
-          const float m_tile = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
+              mx4[(c >> 1) & 3] = fmax3_nan(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          }
+          float m_tile = fmax3_nan(fmax3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]) * sc;
+          if (m_tile != m_tile) {  // a NaN among the kept keys: the row's result is NaN
+            row_nan = true;
+            m_tile = first ? 0.f : m_run;
+          }
           float alpha = 1.0f;
           bool rescale = false;
           if (first) {
@@ -593,12 +668,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
             }
           }
           const float m_use = m_run == -INFINITY ? 0.f : m_run;
-          // ---- P: keys 64.. from registers, then keys 0..63 loaded again (P lies over S's upper half)
+          // ---- P: keys 64.. (still in registers), then keys 0..63 (P lies over S's upper half)
           float2 sum4[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) sum4[y] = make_float2(0.f, 0.f);
           const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
-          auto weigh = [&]() {
+#pragma unroll 1
+          for (int hf = 1;; --hf) {
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               const float2 v = f2_fma(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, nm2);
@@ -606,12 +682,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
               sum4[(c >> 1) & 3] = f2_add(sum4[(c >> 1) & 3], e);
               s[c >> 1] = pack_half2(e.x, e.y);
             }
-          };
-          weigh();
-          tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-          load_half(0);
-          weigh();
-          tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_st32(tP + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            if (hf == 0) break;
+            load_half(0);
+          }
           l_run += ((sum4[0].x + sum4[0].y) + (sum4[1].x + sum4[1].y)) + ((sum4[2].x + sum4[2].y) + (sum4[3].x + sum4[3].y));
           if (rescale) {  // this tile's S was issued behind the last P V, which is therefore complete
 #pragma unroll 1
@@ -633,9 +707,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         }
         if (!ok) break;
         // ---- output
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar->pv_done[w], (g - 1) & 1, p.err, abort_flag)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], (g - 1) & 1, p.err, abort_flag)))) break;
         tc_fence_after();
-        const bool none = m_run == -INFINITY && !(l_run != l_run);
+        if (row_nan) l_run = __uint_as_float(0x7fffffffu);
+        const bool none = m_run == -INFINITY && !row_nan;
         const float f = none ? 0.f : __uint_as_float((uint32_t)bar->ex_v[slot] << 23) / l_run;
         const long long orow = ((long long)(it.q.tok0 + tok) * p.Hq + hq) * D;
         uint16_t* out = static_cast<uint16_t*>(p.o) + orow;
@@ -661,7 +736,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         if (live && p.lse)
           p.lse[(long long)(it.q.tok0 + tok) * p.Hq + hq] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
         // ---- NaN among the values, rare: the row looks for the keys it keeps that have one
-        if (live && *const_cast<volatile int*>(&bar->nan[slot])) {
+        if (live && bar->nan[slot]) {
           const int32_t* table = p.table + (long long)it.seq * p.max_pages;
           for (int j = 0; j <= pos; ++j) {
             const int id = __ldg(table + (j >> p.log_page));
