@@ -2,12 +2,13 @@
 //
 // The mathematics is that of k_paged_attn.cu; here the products bound the call (4 d flops per kept
 // pair), so the stored numbers are turned into fp16 operands in shared memory once for 256 query rows:
-// one CTA takes two tiles of 128 (token, head in group) rows of one KV head. For 128 keys at a time
+// one CTA takes two tiles of 128 (token, head in group) rows of one KV head. For 64 keys at a time
 //   S_w = Q_w K^T       (tcgen05.mma, fp16 operands K-major in shared memory, fp32 in TMEM)
-//   P_w = 2^(S_w c - m) (one thread per row: running maximum, lazily rescaled sums, fp16 P into the
-//                        upper half of S_w's columns)
+//   P_w = 2^(S_w c - m) (one thread per row: running maximum, lazily rescaled sums, fp16 P over S_w)
 //   O_w += P_w V        (A from TMEM, V MN-major in shared memory)
-// for w = 0, 1 in turn, so that the tensor cores work on one row tile while the softmax is in the other.
+// for w = 0, 1 in turn. S_w has two buffers of 64 columns, so that the scores of the next 64 keys are there
+// when a softmax warp has finished these: with one buffer of 128 columns it waited a third of its
+// time for the two products in between (378 us against 300 for 2048 queries over 8192 keys).
 // Warps 0-3 and 4-7: softmax of row tiles 0 and 1; warps 8-11: keys and values; warp 12: MMA issue.
 //
 // Operands. q as fp16 times a power of two per row (exact for bf16 above 2^-28 of the row's largest).
@@ -50,7 +51,7 @@ struct ChunkCfg {
   static constexpr int TILE = KB * BOX;
   static constexpr int NST = 2;
   static constexpr int SMEM_TILES = TILE * (2 + 2 * NST);  // Q x 2, NST x (K, V)
-  static constexpr int COL_S = 0, COL_P = 64, COL_O = 256;  // S_w: 128 w; P_w: + 64; O_w: 256 + D w
+  static constexpr int COL_S = 0, COL_O = 256;  // S_w, buffer b: 128 w + 64 b (P_w over it); O_w: 256 + D w
   static constexpr int THREADS = 416;
 };
 
@@ -62,7 +63,7 @@ struct TileDesc {
 };
 struct ChunkBar {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2], p_ready[2], pv_done[2];
+  uint64_t q_full[2], s_full[2][2], p_ready[2][2], pv_done[2];
   uint64_t conv, drain;
   TileDesc desc[4];
   KeyPut keys[2][128];
@@ -141,6 +142,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, unsigne
   }
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r = 0;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.u32 %0, 1;\n\t}" : "+r"(r));
+  return r != 0;
+}
 // Largest of three, NaN if one is.
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float r;
@@ -190,8 +197,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
       mbar_init(&bar->v_full[s], 128);
       mbar_init(&bar->v_empty[s], 1);
       mbar_init(&bar->q_full[s], 128);
-      mbar_init(&bar->s_full[s], 1);
-      mbar_init(&bar->p_ready[s], 128);
+      mbar_init(&bar->s_full[s][0], 1);
+      mbar_init(&bar->s_full[s][1], 1);
+      mbar_init(&bar->p_ready[s][0], 128);
+      mbar_init(&bar->p_ready[s][1], 128);
       mbar_init(&bar->pv_done[s], 1);
     }
     mbar_init(&bar->conv, 128);
@@ -481,57 +490,60 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         if (last) break;
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp == 12) {
     // ------------------------------------------------------------ MMA issue
-    if (warp == 12 && lane == 0) {
-      constexpr uint32_t idS = make_idesc_f16(128, 128, false), idO = make_idesc_f16(128, D, true);
+    if (elect_one()) {
+      constexpr uint32_t idS = make_idesc_f16(128, 64, false), idO = make_idesc_f16(128, D, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
       bool ok = true;
       int g = 0, item = 0;
-      auto issue_S = [&](int w, int gg) {
-        const uint32_t qlo = sdesc_lo(sQa + w * C::TILE, 16), klo = sdesc_lo(sKa + (gg % NST) * C::TILE, 16);
+      // scores of half tile u = 2 g + half (64 keys)
+      auto issue_S = [&](int w, int u) {
+        const uint32_t qlo = sdesc_lo(sQa + w * C::TILE, 16);
+        const uint32_t klo = sdesc_lo(sKa + ((u >> 1) % NST) * C::TILE + (u & 1) * 64 * 128, 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + C::COL_S + w * 128, sdesc_join(qlo + off, kDescHi), sdesc_join(klo + off, kDescHi), idS,
-                 kk > 0 ? 1u : 0u);
+          mma_ss(tmem + C::COL_S + w * 128 + (u & 1) * 64, sdesc_join(qlo + off, kDescHi), sdesc_join(klo + off, kDescHi),
+                 idS, kk > 0 ? 1u : 0u);
         }
-        tc_commit(&bar->s_full[w]);
+        tc_commit(&bar->s_full[w][u & 1]);
       };
       for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, ++item) {
         if (!(ok = wait_bar(&bar->q_full[0], item & 1, p.err, abort_flag))) break;
         if (!(ok = wait_bar(&bar->q_full[1], item & 1, p.err, abort_flag))) break;
         if (!(ok = wait_bar(&bar->k_full[g % NST], (g / NST) & 1, p.err, abort_flag))) break;
         tc_fence_after();
-        for (int w = 0; w < 2; ++w) issue_S(w, g);
+        for (int z = 0; z < 4; ++z) issue_S(z & 1, 2 * g + (z >> 1));
         tc_commit(&bar->k_empty[g % NST]);
         bool first = true;
         while (ok) {
           const int st = g % NST;
           const bool last = bar->desc[g & 3].last != 0;
-          for (int w = 0; w < 2; ++w) {
-            if (!(ok = wait_bar(&bar->p_ready[w], g & 1, p.err, abort_flag))) break;
-            if (w == 0 && !(ok = wait_bar(&bar->v_full[st], (g / NST) & 1, p.err, abort_flag))) break;
+#pragma unroll 1
+          for (int z = 0; z < 4; ++z) {  // half z / 2, row tile z % 2
+            const int w = z & 1, u = 2 * g + (z >> 1);
+            if (!(ok = wait_bar(&bar->p_ready[w][u & 1], g & 1, p.err, abort_flag))) break;
+            if (z == 0 && !(ok = wait_bar(&bar->v_full[st], (g / NST) & 1, p.err, abort_flag))) break;
             tc_fence_after();
-            const uint32_t aP = tmem + C::COL_S + w * 128 + C::COL_P;
-            const uint32_t vlo = sdesc_lo(sVa + st * C::TILE, C::BOX);
+            const uint32_t aP = tmem + C::COL_S + w * 128 + (u & 1) * 64;
+            const uint32_t vlo = sdesc_lo(sVa + st * C::TILE + (u & 1) * 64 * 128, C::BOX);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               mma_ts(tmem + C::COL_O + w * D, aP + kk * 8, sdesc_join(vlo + kk * (2048 >> 4), kDescHi), idO,
                      (!first || kk > 0) ? 1u : 0u);
             tc_commit(&bar->pv_done[w]);
-            if (w == 1) tc_commit(&bar->v_empty[st]);
+            if (z == 3) tc_commit(&bar->v_empty[st]);
+            if (w == 1) first = false;
             if (!last) {
-              const int gn = g + 1;
-              if (w == 0) {
-                if (!(ok = wait_bar(&bar->k_full[gn % NST], (gn / NST) & 1, p.err, abort_flag))) break;
+              if (z == 0) {
+                if (!(ok = wait_bar(&bar->k_full[(g + 1) % NST], ((g + 1) / NST) & 1, p.err, abort_flag))) break;
                 tc_fence_after();
               }
-              issue_S(w, gn);
-              if (w == 1) tc_commit(&bar->k_empty[gn % NST]);
+              issue_S(w, u + 2);
+              if (z == 3) tc_commit(&bar->k_empty[(g + 1) % NST]);
             }
           }
-          first = false;
           ++g;
           if (last) break;
         }
@@ -543,7 +555,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     // ------------------------------------------------------------ softmax, one row per thread
     const int w = warp >> 2, row = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::COL_S + w * 128, tP = tS + C::COL_P, tO = tmem + lane_off + C::COL_O + w * D;
+    const uint32_t tS = tmem + lane_off + C::COL_S + w * 128, tO = tmem + lane_off + C::COL_O + w * D;
     bool ok = true;
     int g = 0, slot = 0;
     for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
@@ -592,16 +604,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         const float down = __uint_as_float((uint32_t)(127 - sh) << 23);
         float sc = 0.f, m_run = -INFINITY, l_run = 0.f;
         bool first = true, row_nan = false;
-        for (;;) {
-          if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->s_full[w], g & 1, p.err, abort_flag)))) break;
-          tc_fence_after();
+        for (bool last = false; !last; ++g) {
+          if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->s_full[w][0], g & 1, p.err, abort_flag)))) break;
           const TileDesc* ds = &bar->desc[g & 3];
           if (first) {  // never 0, so that a masked score stays -inf (keys that all are 0: any factor)
             const int ek = bar->ex_k[slot];
             sc = fmaxf(p.scale_log2 * down * (ek ? __uint_as_float((uint32_t)ek << 23) : 1.f), 1.17549435e-38f);
           }
           const int k0 = ds->k0;
-          const bool last = ds->last != 0;
+          last = ds->last != 0;
           uint32_t keep[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) keep[y] = ds->valid[y];
@@ -618,63 +629,60 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
             for (int y = 0; y < 4; ++y) keep[y] = 0;
           }
           const bool mask = __any_sync(0xffffffffu, !full);
-          // ---- masked scores become -inf in place (few tiles: the loops below stay short, they have to
-          // fit the instruction cache beside the other roles)
-          if (mask) {
-#pragma unroll 1
-            for (int y = 0; y < 4; ++y) {
-              uint32_t s[32];
-              tmem_ld32(tS + y * 32, s);
-              tmem_ld_wait();
-              const uint32_t kw = y == 0 ? keep[0] : y == 1 ? keep[1] : y == 2 ? keep[2] : keep[3];
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!((kw >> c) & 1u)) s[c] = 0xff800000u;
-              tmem_st32(tS + y * 32, s);
-            }
-            tmem_st_wait();
-          }
-          // ---- row maximum
-          uint32_t s[64];
-          auto load_half = [&](int hf) {
-            tmem_ld32(tS + hf * 64, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld32(tS + hf * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-            tmem_ld_wait();
-          };
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
-            load_half(hf);
+            const uint32_t tB = tS + hf * 64;
+            if (hf == 1 && !(ok = __all_sync(0xffffffffu, wait_bar(&bar->s_full[w][1], g & 1, p.err, abort_flag)))) break;
+            tc_fence_after();
+            // ---- masked scores become -inf in place (few tiles: the main path stays short, it has to fit the
+            // instruction cache beside the other roles)
+            if (mask) {
+#pragma unroll 1
+              for (int y = 0; y < 2; ++y) {
+                uint32_t s[32];
+                tmem_ld32(tB + y * 32, s);
+                tmem_ld_wait();
+                const uint32_t kw = hf == 0 ? (y == 0 ? keep[0] : keep[1]) : (y == 0 ? keep[2] : keep[3]);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!((kw >> c) & 1u)) s[c] = 0xff800000u;
+                tmem_st32(tB + y * 32, s);
+              }
+              tmem_st_wait();
+            }
+            // ---- row maximum
+            uint32_t s[64];
+            tmem_ld32(tB, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tB + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_ld_wait();
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < 64; c += 2)
               mx4[(c >> 1) & 3] = fmax3_nan(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          }
-          float m_tile = fmax3_nan(fmax3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]) * sc;
-          if (m_tile != m_tile) {  // a NaN among the kept keys: the row's result is NaN
-            row_nan = true;
-            m_tile = first ? 0.f : m_run;
-          }
-          float alpha = 1.0f;
-          bool rescale = false;
-          if (first) {
-            m_run = m_tile;
-          } else {
-            const bool need = m_tile > m_run + 8.0f;
-            rescale = __any_sync(0xffffffffu, need);
-            if (need) {
-              alpha = ex2(m_run - m_tile);
-              l_run *= alpha;
-              m_run = m_tile;
+            float m_tile = fmax3_nan(fmax3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]) * sc;
+            if (m_tile != m_tile) {  // a NaN among the kept keys: the row's result is NaN
+              row_nan = true;
+              m_tile = first ? 0.f : m_run;
             }
-          }
-          const float m_use = m_run == -INFINITY ? 0.f : m_run;
-          // ---- P: keys 64.. (still in registers), then keys 0..63 (P lies over S's upper half)
-          float2 sum4[4];
+            float alpha = 1.0f;
+            bool rescale = false;
+            if (first) {
+              m_run = m_tile;
+            } else {
+              const bool need = m_tile > m_run + 8.0f;
+              rescale = __any_sync(0xffffffffu, need);
+              if (need) {
+                alpha = ex2(m_run - m_tile);
+                l_run *= alpha;
+                m_run = m_tile;
+              }
+            }
+            const float m_use = m_run == -INFINITY ? 0.f : m_run;
+            // ---- P
+            float2 sum4[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) sum4[y] = make_float2(0.f, 0.f);
-          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
-#pragma unroll 1
-          for (int hf = 1;; --hf) {
+            for (int y = 0; y < 4; ++y) sum4[y] = make_float2(0.f, 0.f);
+            const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               const float2 v = f2_fma(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, nm2);
@@ -682,32 +690,33 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
               sum4[(c >> 1) & 3] = f2_add(sum4[(c >> 1) & 3], e);
               s[c >> 1] = pack_half2(e.x, e.y);
             }
-            tmem_st32(tP + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            if (hf == 0) break;
-            load_half(0);
-          }
-          l_run += ((sum4[0].x + sum4[0].y) + (sum4[1].x + sum4[1].y)) + ((sum4[2].x + sum4[2].y) + (sum4[3].x + sum4[3].y));
-          if (rescale) {  // this tile's S was issued behind the last P V, which is therefore complete
+            l_run += ((sum4[0].x + sum4[0].y) + (sum4[1].x + sum4[1].y)) + ((sum4[2].x + sum4[2].y) + (sum4[3].x + sum4[3].y));
+            tmem_st32(tB, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            if (rescale) {  // behind the last P V (its successor waits for this thread)
+              if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], hf ^ 1, p.err, abort_flag)))) break;
+              tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t ov[32];
-              tmem_ld32(tO + cc * 32, ov);
-              tmem_ld_wait();
+              for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t ov[32];
+                tmem_ld32(tO + cc * 32, ov);
+                tmem_ld_wait();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * alpha);
-              tmem_st32(tO + cc * 32, ov);
+                for (int y = 0; y < 32; ++y) ov[y] = __float_as_uint(__uint_as_float(ov[y]) * alpha);
+                tmem_st32(tO + cc * 32, ov);
+              }
             }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bar->p_ready[w][hf]);
+            first = false;
           }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&bar->p_ready[w]);
-          first = false;
-          ++g;
-          if (last) break;
+          if (!ok) break;
         }
         if (!ok) break;
         // ---- output
-        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], (g - 1) & 1, p.err, abort_flag)))) break;
+        // (the last P V but one first: a parity names the phase before the current one only)
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], 0, p.err, abort_flag)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], 1, p.err, abort_flag)))) break;
         tc_fence_after();
         if (row_nan) l_run = __uint_as_float(0x7fffffffu);
         const bool none = m_run == -INFINITY && !row_nan;
