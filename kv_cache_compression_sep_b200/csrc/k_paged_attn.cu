@@ -48,6 +48,11 @@ constexpr int kScan = 256;           // positions of a tile left of the window (
 constexpr int kDense = 64;           // positions of a window tile (every row loaded)
 constexpr int kMaxWarps = 2048;      // workspace slots are laid out for this many
 
+// a / b for a >= 0, b > 0: tile numbers rarely need 64 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Row tile rt covers rows rt * R .. of the sequence's nq * G (token, head in group) rows.
 struct RowTile {
   int w0, kend;  // keys [w0, kend) are loaded whole, keys [0, w0) only where kept by every row
@@ -479,18 +484,32 @@ __device__ __forceinline__ void fetch_run(const PagedAttnParams& p, uint32_t sta
 }
 
 // Keys [c0, c1) of the window part (c0 a multiple of 64), for queries at positions lo .. hi. Two stages
-// of 32 keys: one is computed on while the other arrives.
+// of 32 keys: one is computed on while the other arrives. The first two are requested by window_begin,
+// before the queries are looked at.
+struct Window {
+  PageRun pr;
+  Run32 x, xn;  // this stage's keys and the next one's
+};
+template <int D>
+__device__ __forceinline__ Window window_begin(const PagedAttnParams& p, int seq, int h, int len, int c0, int c1,
+                                               uint32_t ring, int lane) {
+  Window w;
+  w.pr = load_pages(p, seq, h, c0 >> p.log_page, len, lane);
+  w.x = run32(p, w.pr, c0, c1);
+  w.xn = run32(p, w.pr, min(c0 + 32, (c1 - 1) & ~31), c1);
+  fetch_run<D>(p, ring, w.x, lane);
+  if (c0 + 32 < c1) fetch_run<D>(p, ring + Ring<D>::kBytes, w.xn, lane);
+  else copy_commit();
+  return w;
+}
 template <int D, int NT>
-__device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int len,
-                                            int lo, int hi, int c0, int c1, uint32_t ring, int lane) {
+__device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D, NT>& r, const Window& w0, int seq, int h,
+                                            int len, int lo, int hi, int c0, int c1, uint32_t ring, int lane) {
   using C = Ring<D>;
   const int g = lane >> 2, t = lane & 3;
   const int run = 32 << p.log_page;
-  PageRun pr = load_pages(p, seq, h, c0 >> p.log_page, len, lane);
-  Run32 x = run32(p, pr, c0, c1), xn = run32(p, pr, min(c0 + 32, c1 - 1 & ~31), c1);
-  fetch_run<D>(p, ring, x, lane);
-  if (c0 + 32 < c1) fetch_run<D>(p, ring + C::kBytes, xn, lane);
-  else copy_commit();
+  PageRun pr = w0.pr;
+  Run32 x = w0.x, xn = w0.xn;
   uint32_t stage = ring;
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
@@ -558,100 +577,115 @@ __device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D
 }
 
 // ------------------------------------------------------------------ tiles left of the window
-// Positions [c0, c1) (at most kScan, c0 a multiple of kScan): the keys with j < a or a separator flag,
-// kept by every row, are listed in shared memory and read 32 at a time.
+// The positions of tiles y0 .. y1 - 1 (kScan each, up to w0): the keys with j < a or a separator flag, kept
+// by every row, are listed in shared memory, four tiles at a time (their page numbers, flags and scales
+// are requested together), and read 32 at a time.
 struct Listed {
   uint32_t row, ex;  // pool row, exponents of its page's scales
 };
+constexpr int kScanGroup = 4;
 template <int D, int NT>
-__device__ __forceinline__ void scan_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int c0, int c1,
+__device__ __forceinline__ void scan_keys(const PagedAttnParams& p, RowState<D, NT>& r, int seq, int h, int y0, int y1, int w0,
                                           Listed* list, uint32_t ring, int lane) {
   using C = Ring<D>;
   const int g = lane >> 2, t = lane & 3;
-  // kScan / 32 positions per lane: always inside one page
-  constexpr int kPer = kScan / 32;
-  const int j0 = c0 + kPer * lane;
-  uint32_t bits = 0, row = 0, ex = 0;
-  if (j0 < c1) {
-    const int pg = j0 >> p.log_page;
-    const int id = pg < p.max_pages ? __ldg(p.table + (long long)seq * p.max_pages + pg) : -1;
-    if (id >= 0 && id < p.num_pages) {
-      const int off = j0 & ((1 << p.log_page) - 1);
-      const uint2 f = __ldg(reinterpret_cast<const uint2*>(p.flags + ((size_t)id << p.log_page) + off));
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) bits |= (((x < 4 ? f.x : f.y) >> (8 * (x & 3))) & 0xffu ? 1u : 0u) << x;
-      const int init = p.a - j0;  // initial tokens
-      if (init > 0) bits |= init >= kPer ? (1u << kPer) - 1u : (1u << init) - 1u;
-      const int left = c1 - j0;
-      if (left < kPer) bits &= (1u << left) - 1u;
-      const size_t sc = (size_t)id * p.Hkv + h;
-      row = (uint32_t)(sc << p.log_page) + off;
-      ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
-    } else {
-      record_failure(p.err, nullptr, SEP_ERR_INDEX);
-    }
-  }
-  const int cnt = __popc(bits);
-  int at = cnt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += y;
-  }
-  const int total = __shfl_sync(0xffffffffu, at, 31);
-  at -= cnt;
-  __syncwarp();  // the list's last readers are done
-  while (bits) {
-    const int x = __ffs(bits) - 1;
-    bits &= bits - 1;
-    list[at++] = Listed{row + x, ex};
-  }
-  __syncwarp();
-  if (total == 0) return;
-  auto fetch = [&](uint32_t stage, int b) {
-    fetch32<D>(p, stage, lane, [&](int r, bool* on) {
-      *on = b + r < total;
-      return list[min(b + r, total - 1)].row;
-    });
-  };
-  fetch(ring, 0);
-  if (32 < total) fetch(ring + C::kBytes, 32);
-  else copy_commit();
-  uint32_t stage = ring;
+  constexpr int kPer = kScan / 32;  // positions per lane and tile: always inside one page
+  const int32_t* table = p.table + (long long)seq * p.max_pages;
 #pragma unroll 1
-  for (int b = 0; b < total; b += 32) {
-    copy_wait<1>();
-    __syncwarp();
-    float s[NT][2][4], ve[2][2];
-    scores32(r, stage, g, t, s);
+  for (; y0 < y1; y0 += kScanGroup) {
+    int id[kScanGroup];
+    uint32_t bits[kScanGroup], row[kScanGroup], ex[kScanGroup];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int x = b + 16 * i + 8 * u + g;
-        const uint32_t e = list[min(x, total - 1)].ex;
-        ve[i][u] = value_log2(e);
-        const float ks = key_scale(e);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int z = 0; z < 2; ++z)
-            s[nt][i][2 * u + z] = x < total ? s[nt][i][2 * u + z] * (ks * r.qs[nt][z]) : -INFINITY;
+    for (int z = 0; z < kScanGroup; ++z) {
+      const int j0 = (y0 + z) * kScan + kPer * lane;
+      id[z] = y0 + z < y1 && j0 < w0 ? __ldg(table + (j0 >> p.log_page)) : -1;
+      if (y0 + z < y1 && j0 < w0 && (id[z] < 0 || id[z] >= p.num_pages)) {
+        record_failure(p.err, nullptr, SEP_ERR_INDEX);
+        id[z] = -1;
       }
-    uint32_t pb[NT][2][2];
-    weights32(r, s, ve, pb);
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      VFrag<D> vf;
-      load_v(vf, stage, i, g, t);
-      accumulate16(r, vf, pb, i);
+    for (int z = 0; z < kScanGroup; ++z) {
+      bits[z] = row[z] = ex[z] = 0;
+      if (id[z] >= 0) {
+        const int j0 = (y0 + z) * kScan + kPer * lane, off = j0 & ((1 << p.log_page) - 1);
+        const uint2 f = __ldg(reinterpret_cast<const uint2*>(p.flags + ((size_t)id[z] << p.log_page) + off));
+        const size_t sc = (size_t)id[z] * p.Hkv + h;
+        row[z] = (uint32_t)(sc << p.log_page) + off;
+        ex[z] = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) bits[z] |= (((x < 4 ? f.x : f.y) >> (8 * (x & 3))) & 0xffu ? 1u : 0u) << x;
+        const int init = p.a - j0;  // initial tokens
+        if (init > 0) bits[z] |= init >= kPer ? (1u << kPer) - 1u : (1u << init) - 1u;
+      }
+    }
+    __syncwarp();  // the list's last readers are done
+    int total = 0;
+#pragma unroll
+    for (int z = 0; z < kScanGroup; ++z) {
+      const int cnt = __popc(bits[z]);
+      int at = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += y;
+      }
+      const int sum = __shfl_sync(0xffffffffu, at, 31);
+      at += total - cnt;
+      while (bits[z]) {
+        const int x = __ffs(bits[z]) - 1;
+        bits[z] &= bits[z] - 1;
+        list[at++] = Listed{row[z] + x, ex[z]};
+      }
+      total += sum;
     }
     __syncwarp();
-    if (b + 64 < total) fetch(stage, b + 64);
+    if (total == 0) continue;
+    auto fetch = [&](uint32_t stage, int b) {
+      fetch32<D>(p, stage, lane, [&](int r, bool* on) {
+        *on = b + r < total;
+        return list[min(b + r, total - 1)].row;
+      });
+    };
+    fetch(ring, 0);
+    if (32 < total) fetch(ring + C::kBytes, 32);
     else copy_commit();
-    stage = stage == ring ? ring + C::kBytes : ring;
+    uint32_t stage = ring;
+#pragma unroll 1
+    for (int b = 0; b < total; b += 32) {
+      copy_wait<1>();
+      __syncwarp();
+      float s[NT][2][4], ve[2][2];
+      scores32(r, stage, g, t, s);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int x = b + 16 * i + 8 * u + g;
+          const uint32_t e = list[min(x, total - 1)].ex;
+          ve[i][u] = value_log2(e);
+          const float ks = key_scale(e);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              s[nt][i][2 * u + z] = x < total ? s[nt][i][2 * u + z] * (ks * r.qs[nt][z]) : -INFINITY;
+        }
+      uint32_t pb[NT][2][2];
+      weights32(r, s, ve, pb);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        VFrag<D> vf;
+        load_v(vf, stage, i, g, t);
+        accumulate16(r, vf, pb, i);
+      }
+      __syncwarp();
+      if (b + 64 < total) fetch(stage, b + 64);
+      else copy_commit();
+      stage = stage == ring ? ring + C::kBytes : ring;
+    }
+    copy_wait<0>();
   }
-  copy_wait<0>();
 }
 
 // ------------------------------------------------------------------ kernel
@@ -662,9 +696,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
   __shared__ long long s_part[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(s_raw) + warp * (Ring<D>::kStages * Ring<D>::kBytes);
-  Listed* list = reinterpret_cast<Listed*>(s_raw + kWarps * Ring<D>::kStages * Ring<D>::kBytes) + warp * kScan;
+  Listed* list = reinterpret_cast<Listed*>(s_raw + kWarps * Ring<D>::kStages * Ring<D>::kBytes) + warp * (kScanGroup * kScan);
   long long* s_base = reinterpret_cast<long long*>(s_raw + kWarps * (Ring<D>::kStages * Ring<D>::kBytes +
-                                                                     kScan * (int)sizeof(Listed)));  // [S + 1]
+                                                                     kScanGroup * kScan * (int)sizeof(Listed)));  // [S + 1]
   grid_dep_wait();
   grid_dep_launch_next();
 
@@ -711,7 +745,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
         for (long long e = lane; e < cnt; e += 32) p.lse[at + e] = -INFINITY;
     }
   }
-  const long long per = (total + p.nwarps - 1) / p.nwarps;
+  const long long per = quotient(total + p.nwarps - 1, p.nwarps);
   long long x = (long long)gw * per;
   const long long x_end = min(total, x + per);
   if (x >= x_end) return;
@@ -731,20 +765,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
     while (s_base[seq + 1] <= x) ++seq;
     const SeqInfo q = seq_info(p, seq);
     const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
-    const long long unit = (x - s_base[seq]) / per_rt;
+    const long long unit = quotient(x - s_base[seq], per_rt);
     const int ta = (int)((x - s_base[seq]) - unit * per_rt);
     const int tb = (int)min((long long)per_rt, ta + (x_end - x));
-    const int h = (int)(unit / nrt), rt = (int)(unit - (long long)h * nrt);
+    const int h = (int)quotient(unit, nrt), rt = (int)(unit - (long long)h * nrt);
     const RowTile w = row_tile(p, q, rt, R);
-    begin_rows<D, NT>(p, r, q, h, rt, g, t);
-    for (int y = ta; y < min(tb, w.ns); ++y)
-      scan_keys<D, NT>(p, r, seq, h, y * kScan, min(w.w0, (y + 1) * kScan), list, ring, lane);
     const int da = max(ta, w.ns) - w.ns, db = min(tb - w.ns, w.nd);
+    const int c0 = w.w0 + da * kDense, c1 = min(w.kend, w.w0 + db * kDense);
+    Window win;
+    if (ta >= w.ns && da < db) win = window_begin<D>(p, seq, h, q.len, c0, c1, ring, lane);
+    begin_rows<D, NT>(p, r, q, h, rt, g, t);
+    if (ta < w.ns) {
+      scan_keys<D, NT>(p, r, seq, h, ta, min(tb, w.ns), w.w0, list, ring, lane);
+      if (da < db) win = window_begin<D>(p, seq, h, q.len, c0, c1, ring, lane);
+    }
     if (da < db) {
       const int lo = q.lead + rt * R / p.G;
       const int hi = q.lead + min(q.nq - 1, (rt * R + R - 1) / p.G);
-      window_keys<D, NT>(p, r, seq, h, q.len, lo, hi, w.w0 + da * kDense,
-                         min(w.kend, w.w0 + db * kDense), ring, lane);
+      window_keys<D, NT>(p, r, win, seq, h, q.len, lo, hi, c0, c1, ring, lane);
     }
     const bool whole = ta == 0 && tb == per_rt;
     // a warp's run has at most one row tile that began before it (slot 0) and one that ends after it
@@ -774,7 +812,7 @@ __device__ __forceinline__ void join_row(const PagedAttnParams& p, JoinShared<D>
   constexpr int R = 8 * NT, LPR = JoinShared<D>::LPR, GR = JoinShared<D>::GR;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lr = row % R, tok = q.tok0 + row / p.G, hq = h * p.G + row % p.G;
-  const int w0 = (int)(t0 / per), w1 = (int)((t1 - 1) / per), parts = w1 - w0 + 1;
+  const int w0 = (int)quotient(t0, per), w1 = (int)quotient(t1 - 1, per), parts = w1 - w0 + 1;
   if (parts == 1) return;
   const int first_slot = t0 > (long long)w0 * per ? 1 : 0;
   auto part = [&](int i) -> const float* { return part_of<D, R>(p, w0 + i, i == 0 ? first_slot : 0); };
@@ -847,6 +885,93 @@ __device__ __forceinline__ void join_row(const PagedAttnParams& p, JoinShared<D>
   }
 }
 
+// The same by one warp (many rows of few parts each).
+template <int D, int NT>
+__device__ __forceinline__ void join_row_warp(const PagedAttnParams& p, const SeqInfo& q, int h, int row, long long t0,
+                                              long long t1, long long per) {
+  constexpr int R = 8 * NT, F = D / 32;  // columns per lane
+  const int lane = threadIdx.x & 31;
+  const int lr = row % R, tok = q.tok0 + row / p.G, hq = h * p.G + row % p.G;
+  const int w0 = (int)quotient(t0, per), w1 = (int)quotient(t1 - 1, per), parts = w1 - w0 + 1;
+  if (parts == 1) return;
+  const int first_slot = t0 > (long long)w0 * per ? 1 : 0;
+  auto part = [&](int i) -> const float* { return part_of<D, R>(p, w0 + i, i == 0 ? first_slot : 0); };
+  auto stats = [&](int i) { return *reinterpret_cast<const float4*>(part(i) + (size_t)R * D + lr * 4); };
+  float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);  // of part `lane`
+  if (lane < parts) st = stats(lane);
+  float mo = st.x, m = st.y;
+  for (int i = lane + 32; i < parts; i += 32) {
+    const float4 y = stats(i);
+    mo = fmaxf(mo, y.x);
+    m = fmaxf(m, y.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  const float mor = mo == -INFINITY ? 0.f : mo, mr = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[F];
+#pragma unroll
+  for (int y = 0; y < F; ++y) acc[y] = 0.f;
+  for (int b = 0; b < parts; b += 32) {
+    if (b > 0) st = b + lane < parts ? stats(b + lane) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    const float f = ex2(st.x - mor);
+    l += b + lane < parts ? st.z * ex2(st.y - mr) : 0.f;
+    const int n = min(32, parts - b);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* a = part(b + i) + (size_t)lr * D + lane * F;
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      if (F == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(a);
+        acc[0] = fmaf(v.x, fi, acc[0]);
+        acc[1] = fmaf(v.y, fi, acc[1]);
+        acc[F - 2] = fmaf(v.z, fi, acc[F - 2]);
+        acc[F - 1] = fmaf(v.w, fi, acc[F - 1]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(a);
+        acc[0] = fmaf(v.x, fi, acc[0]);
+        acc[1] = fmaf(v.y, fi, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const bool none = m == -INFINITY && !(l != l);
+  float2 f = join_factors(mo, m, l);
+  if (none || mo == -INFINITY) f = make_float2(0.f, none ? 0.f : 1.f / l);
+  const long long at = ((long long)tok * p.Hq + hq) * D + lane * F;
+#pragma unroll
+  for (int y = 0; y < F; y += 2)
+    store_out(p, at + y, none ? 0.f : acc[y] * f.x * f.y, none ? 0.f : acc[y + 1] * f.x * f.y);
+  if (lane == 0 && p.lse) p.lse[(long long)tok * p.Hq + hq] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+template <int D, int NT>
+__global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int R = 8 * NT;
+  const int lane = threadIdx.x & 31, x = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int tok = x / p.Hq, hq = x - tok * p.Hq;
+  grid_dep_wait();
+  grid_dep_launch_next();
+  if (tok >= p.T) return;
+  // sequence of the token: last s with indptr[s] <= tok
+  int seq = -1;
+  for (int s0 = 0; s0 < p.S; s0 += 32) {
+    const int hit = __popc(__ballot_sync(0xffffffffu, s0 + lane < p.S && __ldg(p.indptr + min(s0 + lane, p.S)) <= tok));
+    seq += hit;
+    if (hit < min(32, p.S - s0)) break;
+  }
+  if (seq < 0) return;
+  const long long base = p.base[seq], total = p.base[p.S];
+  const SeqInfo q = seq_info(p, seq);
+  if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
+  const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
+  const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+  const long long t0 = base + ((long long)h * nrt + row / R) * per_rt;
+  join_row_warp<D, NT>(p, q, h, row, t0, t0 + per_rt, quotient(total + p.nwarps - 1, p.nwarps));
+}
+
 // One CTA per (query token, query head); where chunks are present (and most tokens belong to them), one
 // per boundary between two warps' runs, for the row tile that it cuts first.
 template <int D, int NT>
@@ -897,23 +1022,26 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 template <int D, int NT>
 cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
   const size_t smem = (size_t)(p.S + 1) * sizeof(long long) +
-                      (size_t)kWarps * (kScan * sizeof(Listed) + Ring<D>::kStages * Ring<D>::kBytes);
+                      (size_t)kWarps * (kScanGroup * kScan * sizeof(Listed) + Ring<D>::kStages * Ring<D>::kBytes);
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !set[dev].load()) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev].store(true);
   }
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_attn_kernel<D, NT>, kWarps * 32, smem);
-  if (e != cudaSuccess) return e;
-  const int grid = std::min(kMaxWarps / kWarps, 148 * std::max(per_sm, 1));
+  const int grid = 148 * kCtasPerSm;
+  static_assert(148 * kCtasPerSm * kWarps <= kMaxWarps, "workspace slots");
   p.nwarps = grid * kWarps;
   e = launch_chained(paged_attn_kernel<D, NT>, dim3(grid), dim3(kWarps * 32), smem, stream, p);
   if (e != cudaSuccess) return e;
+  // A warp per row once the rows fill the SMs with warps; 64 x 800 tokens, 32 heads: 37 us with a CTA per
+  // row. Few rows are joined by a CTA each, whose warps share the parts.
+  if (!p.chunks && (long long)p.T * p.Hq >= 1024)
+    return launch_chained(paged_join_rows_kernel<D, NT>, dim3((unsigned)(((long long)p.T * p.Hq + 3) / 4)), dim3(128), 0,
+                          stream, p);
   return launch_chained(paged_join_kernel<D, NT>, dim3(p.chunks ? (unsigned)p.nwarps : (unsigned)p.T * p.Hq),
                         dim3(kJoinThreads), 0, stream, p);
 }
