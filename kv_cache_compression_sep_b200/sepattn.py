@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 import struct
@@ -423,6 +424,9 @@ _ROPE_TENSOR = struct.Struct("@PP6qi4x")    # SepRopeTensor
 _PAGED = struct.Struct("@4i5PPiif4x")       # SepPagedState
 
 
+_CONTIGUOUS = torch.contiguous_format
+
+
 def _raw_stream(device_index):
     """The current stream of a device as an integer handle."""
     return torch._C._cuda_getCurrentRawStream(device_index)
@@ -434,7 +438,7 @@ def _one_device(first, *rest):
     for t in rest:
         if t is not None and t.get_device() != dev:
             raise SepError(f"a tensor of the call is on {t.device}, the others on {first.device}")
-    if dev != _current_device_index():
+    if dev != torch._C._cuda_getDevice():
         raise SepError(f"the call's tensors are on {first.device} but the current CUDA device is "
                        f"cuda:{_current_device_index()}; make {first.device} current "
                        "(torch.cuda.device) for this call")
@@ -562,7 +566,7 @@ def _rope_side(name, t, lead, nd, dtype, y):
     if not isinstance(t, torch.Tensor) or t.dim() != nd:
         raise SepError(f"{name} must be a {nd}-D tensor")
     shape, st = t.shape, t.stride()
-    if tuple(shape[:-2]) != tuple(lead):
+    if shape[:-2] != lead:
         raise SepError(f"{name} has shape {tuple(shape)}, expected {tuple(lead)} + (heads, d)")
     if t.dtype is not dtype:
         raise SepError(f"{name} has dtype {t.dtype}, q has {dtype}")
@@ -572,9 +576,8 @@ def _rope_side(name, t, lead, nd, dtype, y):
         raise SepError(f"{name} must be on a CUDA device (there is no CPU path)")
     ptr = t.data_ptr()
     if y is None:
-        y = torch.empty_like(t, memory_format=torch.contiguous_format)
-        ys = y.stride()
-        yptr = y.data_ptr()
+        y = torch.empty_like(t, memory_format=_CONTIGUOUS)
+        ys, yptr = y.stride(), y.data_ptr()
     else:
         _strided(y, (dtype,), f"out {name}", shape)
         ys = y.stride()
@@ -604,7 +607,8 @@ def _rope_call(fn, what, q, k, positions, rope, out):
         raise SepError(f"d_rot = {rope.d_rot} is larger than the head dimension {d}")
     if k is not None and isinstance(k, torch.Tensor) and k.shape[-1] != d:
         raise SepError(f"k has head dimension {k.shape[-1]}, q has {d}")
-    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+    pos_type = positions.dtype if isinstance(positions, torch.Tensor) else None
+    if pos_type is not torch.int32 and pos_type is not torch.int64:
         raise SepError("positions must be an int32 or int64 tensor")
     if positions.shape != lead and positions.shape != lead[-1:]:
         raise SepError(f"positions has shape {tuple(positions.shape)}, expected {tuple(lead)} "
@@ -634,7 +638,7 @@ def _rope_call(fn, what, q, k, positions, rope, out):
     if B * L > INT32_MAX:
         raise SepError("more than 2^31 - 1 tokens")
     _check(fn(rope._packed(), code, B, L, d, positions.data_ptr(),
-              1 if positions.dtype is torch.int64 else 0,
+              1 if pos_type is torch.int64 else 0,
               L if nd == 4 and positions.dim() == 2 else 0, qa, ka, _raw_stream(dev)), what)
     return yq, yk
 
@@ -793,7 +797,7 @@ class SepPagedCache:
         self._state()
         if sep is not None:
             _cuda(sep, torch.uint8, "sep", (T,))
-        dev = _one_device(k, v, page_table, seq_lens, indptr, sep, self.k_pages, self.v_pages,
+        dev = _one_device(self.k_pages, k, v, page_table, seq_lens, indptr, sep, self.v_pages,
                           self.k_scale, self.v_scale, self.flags,
                           self.rope.freq if self.rope is not None else None)
         if T == 0:
@@ -826,16 +830,18 @@ class SepPagedCache:
             raise SepError(f"scale = {scale} must be positive")
         scale = self.d ** -0.5 if scale is None else scale
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = torch.empty_like(q, memory_format=_CONTIGUOUS)
         else:
             _cuda(out, q.dtype, "out", (T, Hq, d))
         if lse is None:
-            lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+            lse = q.new_empty((T, Hq), dtype=torch.float32)
         else:
             _cuda(lse, torch.float32, "lse", (T, Hq))
         dev = _one_device(q, page_table, seq_lens, indptr, out, lse, workspace, self.k_pages,
                           self.v_pages, self.k_scale, self.v_scale, self.flags)
-        ws = _workspace(seppaged_attn_workspace_size(S, self.d), q.device, workspace)
+        nbytes = seppaged_attn_workspace_size(S, self.d)
+        ws = q.new_empty(nbytes, dtype=torch.uint8) if workspace is None else \
+            _workspace(nbytes, q.device, workspace)
         if T == 0:
             return out, lse
         _check(_lib.seppaged_attn(self._packed(), _DTYPES[q.dtype], *row, Hq, T, S, max_pages,
@@ -845,5 +851,6 @@ class SepPagedCache:
         return out, lse
 
 
+@functools.lru_cache(maxsize=None)
 def seppaged_attn_workspace_size(S, d) -> int:
     return int(_lib.seppaged_attn_workspace_size(S, d))
