@@ -46,7 +46,7 @@ constexpr int kWarps = 4;            // per CTA
 constexpr int kCtasPerSm = 2;
 constexpr int kScan = 256;           // positions of a tile left of the window (kept rows are gathered)
 constexpr int kDense = 64;           // positions of a window tile (every row loaded)
-constexpr int kMaxWarps = 2048;      // workspace slots are laid out for this many
+constexpr int kMaxWarps = 148 * kCtasPerSm * kWarps;  // workspace slots are laid out for this many
 
 // a / b for a >= 0, b > 0: tile numbers rarely need 64 bits
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -982,7 +982,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   grid_dep_launch_next();
   const int tid = threadIdx.x;
   if (p.chunks) {
-    const long long total = p.base[p.S], per = (total + p.nwarps - 1) / p.nwarps;
+    const int parts = p.chunk_plan[1], items = p.chunk_plan[0];
+    if (parts > 1)
+      for (int x = blockIdx.x * (kJoinThreads / 32) + tid / 32; x < items * kRowsPerItem; x += gridDim.x * (kJoinThreads / 32))
+        chunk_join_row<D>(p, x / kRowsPerItem, x % kRowsPerItem, parts, tid & 31);
+    const long long total = p.base[p.S], per = quotient(total + p.nwarps - 1, p.nwarps);
     const long long x = (blockIdx.x + 1ll) * per;
     if (x >= total) return;
     int lo = 0, hi = p.S;
@@ -993,9 +997,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
     const SeqInfo q = seq_info(p, lo);
     const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
-    const long long unit = (x - p.base[lo]) / per_rt, t0 = p.base[lo] + unit * per_rt;
-    if (t0 == x || t0 / per != blockIdx.x) return;
-    const int h = (int)(unit / nrt), rt = (int)(unit - (long long)h * nrt);
+    const long long unit = quotient(x - p.base[lo], per_rt), t0 = p.base[lo] + unit * per_rt;
+    if (t0 == x || quotient(t0, per) != blockIdx.x) return;
+    const int h = (int)quotient(unit, nrt), rt = (int)(unit - (long long)h * nrt);
     for (int row = rt * R; row < min(rt * R + R, q.nq * p.G); ++row) {
       join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, per);
       __syncthreads();
@@ -1048,11 +1052,23 @@ cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
 
 }  // namespace
 
-// Workspace: [S + 1] tile numbers, then two parts per warp (32-row tiles at most).
-size_t paged_attn_workspace(int S, int d) {
-  const size_t base = ((size_t)(S + 1) * sizeof(long long) + 255) / 256 * 256;
-  return base + (size_t)kMaxWarps * 2 * 16 * (d + 4) * sizeof(float);
+// Workspace: [S + 1] tile numbers, [S + 3] plan of the chunks, two parts per warp (16 rows at most), parts of
+// the chunks.
+namespace {
+struct PagedWs {
+  size_t plan, part, chunk, total;
+};
+PagedWs paged_ws(int S, int d) {
+  PagedWs w;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  w.plan = up((size_t)(S + 1) * sizeof(long long));
+  w.part = w.plan + up((size_t)(S + 3) * sizeof(int));
+  w.chunk = w.part + up((size_t)kMaxWarps * 2 * 16 * (d + 4) * sizeof(float));
+  w.total = w.chunk + (size_t)kChunkCtas * kRowsPerItem * (d + 4) * sizeof(float);
+  return w;
 }
+}  // namespace
+size_t paged_attn_workspace(int S, int d) { return paged_ws(S, d).total; }
 
 cudaError_t launch_paged_attn(const SepPagedState& st, int dtype, const void* q, long long q_tok, long long q_head,
                               int Hq, int T, int S, int max_pages, const int32_t* table, const int32_t* lens,
@@ -1073,7 +1089,11 @@ cudaError_t launch_paged_attn(const SepPagedState& st, int dtype, const void* q,
   p.lens = lens;
   p.indptr = indptr;
   p.base = static_cast<long long*>(ws);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)(S + 1) * sizeof(long long) + 255) / 256 * 256);
+  const PagedWs lay = paged_ws(S, st.d);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  p.chunk_plan = reinterpret_cast<int*>(at + lay.plan);
+  p.part = reinterpret_cast<float*>(at + lay.part);
+  p.chunk_part = reinterpret_cast<float*>(at + lay.chunk);
   p.err = device_error_word();
   p.T = T;
   p.S = S;

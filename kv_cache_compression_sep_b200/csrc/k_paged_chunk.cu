@@ -34,9 +34,6 @@ namespace sep {
 
 namespace {
 
-constexpr int kRowsPerItem = 256;
-constexpr int kScanStep = 1024;  // positions examined per refill of the list
-
 struct __align__(8) KeyRow {
   uint32_t row, ex;  // pool row (kNoRow: none), exponent fields of its page's scales
 };
@@ -81,39 +78,6 @@ constexpr int kListCap = 128 + kScanStep;
 template <int D>
 constexpr size_t chunk_smem_bytes(int S) {
   return 1024 + ChunkCfg<D>::SMEM_TILES + sizeof(KeyRow) * kListCap + sizeof(ChunkBar) + sizeof(int) * (S + 2);
-}
-
-// Work item: 256 rows of one sequence and KV head.
-struct Item {
-  SeqInfo q;
-  int seq, h, r0, rows;  // first row, rows of the sequence
-  int w0, kend;          // window keys [w0, kend); listed keys left of w0
-};
-__device__ __forceinline__ int chunk_items(const PagedAttnParams& p, const SeqInfo& q) {
-  if (!is_chunk(p, q)) return 0;
-  return p.Hkv * (int)(((long long)q.nq * p.G + kRowsPerItem - 1) / kRowsPerItem);
-}
-// Item x of the numbering in `base`; within a sequence the latest (longest) rows first.
-__device__ __forceinline__ Item chunk_item(const PagedAttnParams& p, const int* base, int x) {
-  Item it;
-  int lo = 0, hi = p.S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (base[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  it.seq = lo;
-  it.q = seq_info(p, lo);
-  it.rows = it.q.nq * p.G;
-  const int nrt = (it.rows + kRowsPerItem - 1) / kRowsPerItem, y = x - base[lo];
-  const int rt = nrt - 1 - y / p.Hkv;
-  it.h = y % p.Hkv;
-  it.r0 = rt * kRowsPerItem;
-  const int lo_pos = max(0, it.q.lead + it.r0 / p.G);
-  const int hi_pos = it.q.lead + min(it.q.nq - 1, (it.r0 + kRowsPerItem - 1) / p.G);
-  it.kend = max(0, hi_pos + 1);
-  it.w0 = min(max(0, lo_pos - max(p.n, 1) + 1), it.kend) & ~127;
-  return it;
 }
 
 // mbar_wait with long waits left to the hardware: the tries suspend the warp for up to kSuspendNs, so that
@@ -211,11 +175,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
   grid_dep_wait();
   grid_dep_launch_next();
   // ---- first item of every sequence
-  int carry = 0;
+  int carry = 0, steps = 0;
   __syncthreads();
   for (int s0 = 0; s0 < p.S; s0 += C::THREADS) {
     const int s = s0 + tid;
-    const int x = s < p.S ? chunk_items(p, seq_info(p, s)) : 0;
+    int x = 0;
+    if (s < p.S) {
+      const SeqInfo q = seq_info(p, s);
+      x = chunk_items(p, q);
+      if (x > 0) steps = max(steps, chunk_steps(p, q));
+    }
     int inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -232,8 +201,21 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     if (s < p.S) base[s] = before + inc - x;
     __syncthreads();
   }
-  const int nitems = carry;
-  if (tid == 0) base[p.S] = nitems;
+  if (tid == 0) base[p.S] = carry;
+  steps = __reduce_max_sync(0xffffffffu, steps);
+  if (lane == 0) bar->part[warp] = steps;
+  __syncthreads();
+  for (int w = 0; w < C::THREADS / 32; ++w) steps = max(steps, bar->part[w]);
+  // Few items are cut along their keys so that every SM has a part, of four steps at least.
+  const int parts = carry == 0 ? 1 : max(1, min(kChunkCtas / carry, steps / 4));
+  const int nitems = carry * parts;
+  if (blockIdx.x == 0) {
+    for (int s = tid; s <= p.S; s += C::THREADS) p.chunk_plan[2 + s] = base[s];
+    if (tid == 0) {
+      p.chunk_plan[0] = carry;
+      p.chunk_plan[1] = parts;
+    }
+  }
   if ((int)blockIdx.x >= nitems) return;  // no tensor memory was taken
   if (warp == 12) {
     tmem_alloc(&bar->tmem_base, 512);
@@ -259,7 +241,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     };
     int g = 0, slot = 0;
     for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
-      const Item it = chunk_item(p, base, x);
+      const Item it = chunk_item(p, base, x, parts);
       const int32_t* table = p.table + (long long)it.seq * p.max_pages;
       // ---- largest scales of the item's pages
       const int npages = (it.kend + (1 << p.log_page) - 1) >> p.log_page;
@@ -289,7 +271,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         bar->nan[slot] = 0;
       }
       // ---- the tiles: listed keys, then the window
-      int list_at = 0, list_n = 0, scan = 0, win = it.w0;
+      int list_at = 0, list_n = 0, scan = it.scan0, win = it.win0;
       bool any = false;
       // This thread's key of the next tile. Its scales and flag are requested by next_tile and looked at a
       // tile later; its page number is requested a tile earlier still.
@@ -298,20 +280,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
       int e_k0 = -2;  // its window position, -1 listed, -2 no further tile
       int e_flag = 0;
       int id_next = -1;  // page of position win + t
-      if (win + t < it.kend) id_next = __ldg(table + ((win + t) >> p.log_page));
+      if (win + t < it.win1) id_next = __ldg(table + ((win + t) >> p.log_page));
       auto next_tile = [&]() -> bool {
         e_row = kNoRow;
         e_ks = e_vs = 0.f;
         e_ex = 0;
         e_flag = 0;
-        while (list_n - list_at < 128 && scan < it.w0) {
+        while (list_n - list_at < 128 && scan < it.scan1) {
           // what is left moves to the front, then kScanStep more positions are examined, 8 per thread
           const int rem = list_n - list_at;
           const KeyRow keep = t < rem ? list[list_at + t] : KeyRow{0, 0};
           const int j0 = scan + 8 * t;
           uint32_t bits = 0;
           KeyRow first = {0, 0};
-          if (j0 < it.w0) {
+          if (j0 < it.scan1) {
             const int id = __ldg(table + (j0 >> p.log_page));
             if (id >= 0 && id < p.num_pages) {
               const int off = j0 & ((1 << p.log_page) - 1);
@@ -364,12 +346,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           any = true;
           return true;
         }
-        if (win >= it.kend && any) {
+        if (win >= it.win1 && any) {
           e_k0 = -2;
           return true;
         }
         const int j = win + t;
-        if (j < it.kend && id_next >= 0 && id_next < p.num_pages) {
+        if (j < it.win1 && id_next >= 0 && id_next < p.num_pages) {
           const size_t sc = (size_t)id_next * p.Hkv + it.h;
           const int off = j & ((1 << p.log_page) - 1);
           e_row = (uint32_t)(sc << p.log_page) + off;
@@ -379,7 +361,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           if (it.kend - 1 - win >= p.n)
             e_flag = j < p.a ? 1 : (int)__ldg(p.flags + ((size_t)id_next << p.log_page) + off);
         }
-        id_next = j + 128 < it.kend ? __ldg(table + ((j + 128) >> p.log_page)) : -1;
+        id_next = j + 128 < it.win1 ? __ldg(table + ((j + 128) >> p.log_page)) : -1;
         e_k0 = win;
         win += 128;
         any = true;
@@ -559,7 +541,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     bool ok = true;
     int g = 0, slot = 0;
     for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
-      const Item it = chunk_item(p, base, x);
+      const Item it = chunk_item(p, base, x, parts);
       const int r = it.r0 + w * 128 + row;
       const bool live = r < it.rows;
       const int tok = live ? r / p.G : 0, hq = it.h * p.G + (live ? r - tok * p.G : 0);
@@ -720,45 +702,52 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         tc_fence_after();
         if (row_nan) l_run = __uint_as_float(0x7fffffffu);
         const bool none = m_run == -INFINITY && !row_nan;
-        const float f = none ? 0.f : __uint_as_float((uint32_t)bar->ex_v[slot] << 23) / l_run;
-        const long long orow = ((long long)(it.q.tok0 + tok) * p.Hq + hq) * D;
-        uint16_t* out = static_cast<uint16_t*>(p.o) + orow;
+        const float vs = __uint_as_float((uint32_t)bar->ex_v[slot] << 23);
+        const float f = none ? 0.f : vs / l_run;
+        if (parts > 1) {  // this part's own result, for the join
+          float* po = chunk_part_of<D>(p, x);
+          const int pr = w * 128 + row;
 #pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t ov[32];
-          tmem_ld32(tO + cc * 32, ov);
-          tmem_ld_wait();
-          if (live) {
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld32(tO + cc * 32, ov);
+            tmem_ld_wait();
+            if (live) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t pk[4];
+              for (int y = 0; y < 8; ++y)
+                *reinterpret_cast<float4*>(po + (size_t)pr * D + cc * 32 + 4 * y) =
+                    none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                         : make_float4(__uint_as_float(ov[4 * y]) * f, __uint_as_float(ov[4 * y + 1]) * f,
+                                       __uint_as_float(ov[4 * y + 2]) * f, __uint_as_float(ov[4 * y + 3]) * f);
+            }
+          }
+          if (live)
+            *reinterpret_cast<float4*>(po + kRowsPerItem * D + pr * 4) =
+                make_float4(m_run, none ? 0.f : l_run, bar->nan[slot] ? 1.f : 0.f, 0.f);
+        } else {
+          const long long orow = (long long)(it.q.tok0 + tok) * p.Hq + hq;
+          uint16_t* out = static_cast<uint16_t*>(p.o) + orow * D;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld32(tO + cc * 32, ov);
+            tmem_ld_wait();
+            if (live) {
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const float a = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z]) * f;
-                const float b = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z + 1]) * f;
-                pk[z] = p.bf16 ? pack_bf16x2(a, b) : pack_half2(a, b);
+              for (int y = 0; y < 4; ++y) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const float a = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z]) * f;
+                  const float b = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z + 1]) * f;
+                  pk[z] = p.bf16 ? pack_bf16x2(a, b) : pack_half2(a, b);
+                }
+                *reinterpret_cast<uint4*>(out + cc * 32 + 8 * y) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
-              *reinterpret_cast<uint4*>(out + cc * 32 + 8 * y) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
-        }
-        if (live && p.lse)
-          p.lse[(long long)(it.q.tok0 + tok) * p.Hq + hq] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
-        // ---- NaN among the values, rare: the row looks for the keys it keeps that have one
-        if (live && bar->nan[slot]) {
-          const int32_t* table = p.table + (long long)it.seq * p.max_pages;
-          for (int j = 0; j <= pos; ++j) {
-            const int id = __ldg(table + (j >> p.log_page));
-            if (id < 0 || id >= p.num_pages) continue;
-            const int off = j & ((1 << p.log_page) - 1);
-            if (!(pos - j < p.n || j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + off) != 0)) continue;
-            const uint8_t* v = p.v_pages + ((((size_t)id * p.Hkv + it.h) << p.log_page) + off) * D;
-            for (int c = 0; c < D / 4; ++c) {
-              const uint32_t b = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(v) + c));
-              for (int y = 0; y < 4; ++y)
-                if (b >> (8 * y) & 0x80u) out[4 * c + y] = 0x7fffu;  // NaN in bf16 and fp16
-            }
-          }
+          if (live && p.lse) p.lse[orow] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+          if (live && bar->nan[slot]) restore_nan<D>(p, it, pos, out);  // rare
         }
         tc_fence_before();
       }
@@ -785,7 +774,7 @@ cudaError_t launch_chunks_t(const PagedAttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev].store(true);
   }
-  return launch_chained(paged_chunk_kernel<D>, dim3(148), dim3(ChunkCfg<D>::THREADS), smem, stream, p);
+  return launch_chained(paged_chunk_kernel<D>, dim3(kChunkCtas), dim3(ChunkCfg<D>::THREADS), smem, stream, p);
 }
 
 }  // namespace

@@ -623,6 +623,12 @@ def _rope_call(fn, what, q, k, positions, rope, out):
         yq, yk = out[0], out[1] if k is not None else None
         if yq is None:
             raise SepError("out must hold one tensor for each of q and k")
+        if k is not None:
+            for what_else, x, y in (("the other one's input", yk, q), ("the other one's input", yq, k),
+                                    ("each other", yq, yk)):
+                if isinstance(x, torch.Tensor) and isinstance(y, torch.Tensor) and \
+                        x.dim() == nd and y.dim() == nd and _overlap(x, y):
+                    raise SepError(f"the outputs of q and k overlap {what_else}")
     yq, qa = _rope_side("q", q, lead, nd, dtype, yq)
     ka = None
     if k is not None:
@@ -650,24 +656,25 @@ def _extent(t):
 
 
 def _overlap(x, y):
-    """Whether the address ranges of two tensors meet. Views that interleave inside one buffer
-    (q and v of a fused projection) count as overlapping unless their rows cannot meet: same
-    strides and starts that differ by less than the smallest stride hold disjoint rows."""
+    """Whether two tensors may share memory: their address ranges meet, unless both are views of one
+    buffer whose token blocks (heads x d elements) alternate with the same token stride, as the
+    q, k and v of a fused projection do."""
     if x.numel() == 0 or y.numel() == 0:
         return False
     (a0, a1), (b0, b1) = _extent(x), _extent(y)
     if a1 <= b0 or b1 <= a0:
         return False
-    if x.stride() == y.stride() and x.shape[:-2] == y.shape[:-2]:
-        # one token's heads form a block; blocks of x and y alternate with the token stride
+    if x.shape[:-2] == y.shape[:-2] and x.stride()[:-2] == y.stride()[:-2]:
         size = x.element_size()
-        block = ((x.shape[-2] - 1) * x.stride(-2) + x.shape[-1]) * size
+
+        def block(t):
+            return ((t.shape[-2] - 1) * t.stride(-2) + t.shape[-1]) * size
+
         outer = [s * size for n, s in zip(x.shape[:-2], x.stride()[:-2]) if n > 1]
-        if outer:
-            step = min(outer)
+        step = min(outer) if outer else 0
+        if step and all(s % step == 0 for s in outer):
             gap = (b0 - a0) % step
-            if all(s % step == 0 for s in outer) and block <= gap and gap + block <= step:
-                return False
+            return not (block(x) <= gap and gap + block(y) <= step)
     return True
 
 
@@ -833,6 +840,8 @@ class SepPagedCache:
             out = torch.empty_like(q, memory_format=_CONTIGUOUS)
         else:
             _cuda(out, q.dtype, "out", (T, Hq, d))
+            if _overlap(q, out):
+                raise SepError("out overlaps q, which other warps still read")
         if lse is None:
             lse = q.new_empty((T, Hq), dtype=torch.float32)
         else:

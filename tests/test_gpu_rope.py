@@ -113,6 +113,10 @@ def test_transposed_and_expanded_inputs(S):
     check(yk, k, pos.cpu().numpy(), rope, False)
     with pytest.raises(S.SepError, match="expanded"):
         S.sep_rope_fwd(q, k, pos, rope, out=(yq, k))
+    with pytest.raises(S.SepError, match="overlap each other"):
+        S.sep_rope_fwd(q, k, pos, rope, out=(yq, yq[:, :, :3]))
+    with pytest.raises(S.SepError, match="the other one's input"):
+        S.sep_rope_fwd(yq, yk, pos, rope, out=(torch.empty_like(yq), yq[:, :, :3]))
     with pytest.raises(S.SepError, match="overlaps"):
         buf = torch.zeros(2, 32, 6, 64, device="cuda", dtype=torch.float16)
         S.sep_rope_fwd(buf[:, :31], None, pos, rope, out=(buf[:, 1:],))

@@ -106,6 +106,9 @@ def test_address_ranges_of_views():
     q, k, v = buf[:, :, :8], buf[:, :, 8:10], buf[:, :, 10:]
     assert S._overlap(q, q) and S._overlap(q, buf[:, :, 4:])
     assert not S._overlap(k, v) and not S._overlap(v, k)
+    assert not S._overlap(q, k) and not S._overlap(k, q) and not S._overlap(q, v)
+    assert S._overlap(buf[:, :, :9], k) and S._overlap(k, buf[:, :, :9])
+    assert S._overlap(buf[:1, :1, :8], buf[:1, :1, 7:9])
     assert not S._overlap(q, torch.zeros(4))
     assert S._overlap(buf[:, :4], buf[:, 1:])
 
@@ -144,6 +147,18 @@ def _plan(S_=3, pages=2):
     f = FakeCuda
     return (f(torch.zeros(S_, pages, dtype=torch.int32)), f(torch.zeros(S_, dtype=torch.int32)),
             f(torch.zeros(S_ + 1, dtype=torch.int32)))
+
+
+def test_devices_of_a_call(monkeypatch):
+    """Every tensor on one device, and that device the current one."""
+    t = [types.SimpleNamespace(get_device=lambda i=i: i, device=torch.device("cuda", i)) for i in (0, 1)]
+    monkeypatch.setattr(S.torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(S, "_current_device_index", lambda: 0)
+    assert S._one_device(t[0], None, t[0]) == 0
+    with pytest.raises(S.SepError, match="is on cuda:1, the others on cuda:0"):
+        S._one_device(t[0], t[1])
+    with pytest.raises(S.SepError, match="current CUDA device is cuda:0"):
+        S._one_device(t[1], t[1])
 
 
 def test_paged_constructor_refusals():
@@ -195,7 +210,10 @@ def test_attn_binding_refusals(monkeypatch):
     refuses("between", n=-1)
     refuses("at most 4096", plan_=_plan(4097))
     refuses("out has dtype", out=FakeCuda(torch.zeros(3, 4, 64)))
-    refuses("lse has shape", out=q, lse=FakeCuda(torch.zeros(4, 3)))
+    refuses("overlaps q", out=q)
+    refuses("lse has shape", lse=FakeCuda(torch.zeros(4, 3)))
+    refuses("must be positive", scale=0.0)
+    refuses("must be positive", scale=float("nan"))
 
 
 # ------------------------------------------------------------------ C entry points
@@ -258,12 +276,13 @@ def test_append_entry_refusals():
     assert _append(st=_state(rope=_SepRope(None, 64, 0, 1.0))) == INVALID
 
 
-def _attn(st=None, dtype=0, q=P16, Hq=4, T=3, S_=2, a=0, n=8, o=P16, ws=P16, nbytes=1 << 40):
+def _attn(st=None, dtype=0, q=P16, Hq=4, T=3, S_=2, a=0, n=8, scale=1.0, o=P16, ws=P16, nbytes=1 << 40):
     return S._lib.seppaged_attn(ctypes.byref(st or _state()), dtype, q, 256, 64, Hq, T, S_, 2, P16, P16, P16,
-                                a, n, 1.0, o, P16, ws, nbytes, None)
+                                a, n, scale, o, P16, ws, nbytes, None)
 
 
 def test_attn_entry_refusals():
+    assert _attn(scale=0.0) == INVALID and _attn(scale=float("nan")) == INVALID
     assert _attn(Hq=3) == INVALID and _attn(a=-1) == INVALID and _attn(n=-1) == INVALID
     assert _attn(q=None) == INVALID and _attn(o=None) == INVALID
     assert _attn(S_=4097) == UNSUPPORTED and _attn(T=1 << 30) == UNSUPPORTED
