@@ -52,9 +52,10 @@ struct ChunkCfg {
   static constexpr int THREADS = 416;
 };
 
-struct TileDesc {
+struct __align__(16) TileDesc {
   int k0;          // first position of a window tile, -1: listed keys
   int last;        // of the item
+  int holes[2];    // by half tile: keys that do not exist
   uint32_t valid[4];  // keys that exist
   uint32_t anchor[4]; // initial or flagged (window tiles that some row's window does not cover)
 };
@@ -68,7 +69,7 @@ struct ChunkBar {
   // By item modulo 4 (an item's first tile waits for the products of three tiles before, so its slot has
   // been read by then): exponent fields of the largest scales, a NaN among the values.
   int ex_k[4], ex_v[4], nan[4];
-  int red[4], part4[4], any_far[2][4];
+  int red[4], part4[4], any_far[2][4], hole[2][4];
   int part[16];
   uint32_t tmem_base;
   int abort_flag;
@@ -381,18 +382,24 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           bar->keys[g & 1][t] = KeyPut{e_row, fk | fv << 16};
           bar->far[g & 1][t] = fk2 | fv2 << 16;
           const bool w_far = __any_sync(0xffffffffu, (fk2 | fv2 << 16) != kOnes);
-          if (lane == 0) bar->any_far[g & 1][cw] = w_far;
+          if (lane == 0) {
+            bar->any_far[g & 1][cw] = w_far;
+            bar->hole[g & 1][cw] = vmask != 0xffffffffu;
+          }
         }
         if (!(ok = conv_sync())) break;
         // ---- this thread's pieces of the tile's rows: 16 numbers of one row at a time, rows of its warp
-        constexpr int PPR = D / 16, RPI = 32 / PPR, NI = 32 / RPI;  // pieces per row, rows per load, loads
-        const int piece = lane % PPR;
+        // (four lanes take a 64-byte half row, and eight neighbours two rows of one box, so that their
+        // stores touch every bank once)
+        constexpr int NI = D / 16, RPI = 32 / NI;  // loads, rows per load
+        const int quad = lane >> 2, box = D == 128 ? quad >> 1 & 1 : 0, piece = 4 * box + (lane & 3);
+        const int r0 = cw * 32 + (D == 128 ? (quad & 1) + (quad >> 2) * 2 : quad);  // row of load 0
         const bool far = bar->any_far[g & 1][cw] != 0;
         uint4 kx[NI], vx[NI];
         uint32_t fx[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const KeyPut kr = bar->keys[g & 1][cw * 32 + i * RPI + lane / PPR];
+          const KeyPut kr = bar->keys[g & 1][r0 + i * RPI];
           kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
           fx[i] = kr.f;
           if (kr.row != kNoRow) {
@@ -411,9 +418,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         if (t == 0) {
           ds->k0 = k0;
           ds->last = last;
+          ds->holes[0] = bar->hole[g & 1][0] | bar->hole[g & 1][1];
+          ds->holes[1] = bar->hole[g & 1][2] | bar->hole[g & 1][3];
         }
         auto put = [&](uint8_t* tile, int i, const uint4& v, uint32_t sel, bool far) {
-          const int r = cw * 32 + i * RPI + lane / PPR;
+          const int r = r0 + i * RPI;
           const uint32_t f = __byte_perm(fx[i], 0, sel);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t h[8];
@@ -427,13 +436,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
 #pragma unroll
             for (int y = 0; y < 8; ++y) h[y] = hmul2(h[y], f2);
           }
-          // elements 16 piece ..: box piece / 4, chunks 2 (piece % 4) and the next; lanes of the second box
-          // store theirs in the other order, so that eight lanes touch every bank once
-          uint8_t* row = tile + (piece >> 2) * C::BOX + r * 128;
-          const int c0 = (2 * (piece & 3)) ^ (r & 7), second = piece >> 2 & 1;
-          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-          *reinterpret_cast<uint4*>(row + ((c0 ^ second) << 4)) = second ? hi : lo;
-          *reinterpret_cast<uint4*>(row + ((c0 ^ second ^ 1) << 4)) = second ? lo : hi;
+          // elements 16 piece ..: chunks 2 (piece % 4) and the next of the box's row
+          uint8_t* row = tile + box * C::BOX + r * 128;
+          const int c0 = (2 * (lane & 3)) ^ (r & 7);
+          *reinterpret_cast<uint4*>(row + (c0 << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(row + ((c0 ^ 1) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         };
         if (!far) {
 #pragma unroll
@@ -593,24 +600,21 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
             const int ek = bar->ex_k[slot];
             sc = fmaxf(p.scale_log2 * down * (ek ? __uint_as_float((uint32_t)ek << 23) : 1.f), 1.17549435e-38f);
           }
-          const int k0 = ds->k0;
-          last = ds->last != 0;
-          uint32_t keep[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) keep[y] = ds->valid[y];
-          bool full = (keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu;
-          if (k0 >= 0) {
-            full = full && k0 + 127 <= pos && pos - k0 < p.n;
-            if (!full) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) keep[y] &= window_keep_word(y, pos, k0, p.n, kMaxLen, ds->anchor[y]);
-            }
-          } else if (pos < 0) {
-            full = false;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) keep[y] = 0;
-          }
+          const int4 head = *reinterpret_cast<const int4*>(ds);
+          last = head.y != 0;
+          // every row of the warp keeps all 128 keys: none missing, none behind it, none outside its window
+          const bool full = (head.z | head.w) == 0 && pos >= 0 &&
+                            (head.x < 0 || (head.x + 127 <= pos && pos - head.x < p.n));
           const bool mask = __any_sync(0xffffffffu, !full);
+          uint32_t keep[4];
+          if (mask) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              keep[y] = ds->valid[y];
+              if (head.x >= 0) keep[y] &= window_keep_word(y, pos, head.x, p.n, kMaxLen, ds->anchor[y]);
+              if (pos < 0) keep[y] = 0;
+            }
+          }
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t tB = tS + hf * 64;
