@@ -44,6 +44,7 @@ constexpr int kWarps = 4;            // per CTA
 // CTAs per SM. With two, a warp keeps its state in registers and 64 x 8192 tokens take 148 us; three (12
 // warps, 168 registers, a few spills) take 161 us.
 constexpr int kCtasPerSm = 2;
+constexpr int kSeqCache = 512;       // sequences whose index values are kept in shared memory
 constexpr int kScan = 256;           // positions of a tile left of the window (kept rows are gathered)
 constexpr int kDense = 64;           // positions of a window tile (every row loaded)
 constexpr int kMaxWarps = 148 * kCtasPerSm * kWarps;  // workspace slots are laid out for this many
@@ -53,6 +54,18 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// The tiles of a call over W warps: the first `more` warps take one more than the others. A warp's number
+// runs over the CTAs first, so that the longer shares spread over the SMs.
+struct Split {
+  long long each, more;
+  __device__ __forceinline__ Split(long long total, int W) : each(quotient(total, W)), more(total - each * W) {}
+  __device__ __forceinline__ long long start(long long w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int owner(long long t) const {
+    const long long head = more * (each + 1);
+    return (int)(t < head ? quotient(t, each + 1) : more + quotient(t - head, each));
+  }
+};
+
 // Row tile rt covers rows rt * R .. of the sequence's nq * G (token, head in group) rows.
 struct RowTile {
   int w0, kend;  // keys [w0, kend) are loaded whole, keys [0, w0) only where kept by every row
@@ -60,7 +73,8 @@ struct RowTile {
 };
 __device__ __forceinline__ RowTile row_tile(const PagedAttnParams& p, const SeqInfo& q, int rt, int R) {
   RowTile r;
-  const int i_lo = rt * R / p.G, i_hi = min(q.nq - 1, (rt * R + R - 1) / p.G);
+  const int i_lo = rt == 0 ? 0 : rt * R / p.G;
+  const int i_hi = q.nq * p.G <= R ? q.nq - 1 : min(q.nq - 1, (rt * R + R - 1) / p.G);
   const int lo = max(q.lead + i_lo, 0), hi = q.lead + i_hi;
   r.kend = max(0, hi + 1);
   r.w0 = min(max(0, lo - max(p.n, 1) + 1), r.kend) & ~(kDense - 1);
@@ -434,20 +448,21 @@ __device__ __forceinline__ void end_rows(const PagedAttnParams& p, RowState<D, N
 struct PageRun {
   int first;
   uint32_t row;  // first row of the page for this head (id * Hkv + h) * P, kNoRow: none
-  uint32_t ex;   // exponents of its two scales
+  float ks, vs;  // its scales
 };
 __device__ __forceinline__ PageRun load_pages(const PagedAttnParams& p, int seq, int h, int first, int len, int lane) {
   PageRun r;
   r.first = first;
   r.row = kNoRow;
-  r.ex = 0;
+  r.ks = r.vs = 0.f;
   const int pg = first + lane;
   if (pg < p.max_pages && ((long long)pg << p.log_page) < len) {
     const int id = __ldg(p.table + (long long)seq * p.max_pages + pg);
     if (id >= 0 && id < p.num_pages) {
       const size_t sc = (size_t)id * p.Hkv + h;
       r.row = (uint32_t)(sc << p.log_page);
-      r.ex = scale_exponents(__ldg(p.k_scale + sc), __ldg(p.v_scale + sc));
+      r.ks = __ldg(p.k_scale + sc);
+      r.vs = __ldg(p.v_scale + sc);
     } else {
       record_failure(p.err, nullptr, SEP_ERR_INDEX);
     }
@@ -468,11 +483,17 @@ __device__ __forceinline__ Run32 run32(const PagedAttnParams& p, const PageRun& 
     const int x = c0 + 16 * i;
     const int src = ((x >> p.log_page) - pr.first) & 31;
     const uint32_t base = __shfl_sync(0xffffffffu, pr.row, src);
-    r.ex[i] = __shfl_sync(0xffffffffu, pr.ex, src);
     r.row[i] = base + (uint32_t)(x & ((1 << p.log_page) - 1));
     r.left[i] = base == kNoRow ? 0 : max(0, min(16, end - x));
   }
   return r;
+}
+// The scales of the same keys, asked for behind their rows: the first use of a PageRun waits for its loads.
+__device__ __forceinline__ void run32_scales(const PagedAttnParams& p, const PageRun& pr, int c0, Run32& r) {
+  const uint32_t ex = scale_exponents(pr.ks, pr.vs);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r.ex[i] = __shfl_sync(0xffffffffu, ex, (((c0 + 16 * i) >> p.log_page) - pr.first) & 31);
 }
 template <int D>
 __device__ __forceinline__ void fetch_run(const PagedAttnParams& p, uint32_t stage, const Run32& x, int lane) {
@@ -501,6 +522,11 @@ __device__ __forceinline__ Window window_begin(const PagedAttnParams& p, int seq
   if (c0 + 32 < c1) fetch_run<D>(p, ring + Ring<D>::kBytes, w.xn, lane);
   else copy_commit();
   return w;
+}
+// (the rest of window_begin, behind the queries' loads)
+__device__ __forceinline__ void window_scales(const PagedAttnParams& p, Window& w, int c0, int c1) {
+  run32_scales(p, w.pr, c0, w.x);
+  run32_scales(p, w.pr, min(c0 + 32, (c1 - 1) & ~31), w.xn);
 }
 template <int D, int NT>
 __device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D, NT>& r, const Window& w0, int seq, int h,
@@ -568,6 +594,7 @@ __device__ __forceinline__ void window_keys(const PagedAttnParams& p, RowState<D
       if (c + 64 - (pr.first << p.log_page) >= run) pr = load_pages(p, seq, h, (c + 64) >> p.log_page, len, lane);
       xn = run32(p, pr, c + 64, c1);
       fetch_run<D>(p, stage, xn, lane);
+      run32_scales(p, pr, c + 64, xn);
     } else {
       copy_commit();
     }
@@ -699,6 +726,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
   Listed* list = reinterpret_cast<Listed*>(s_raw + kWarps * Ring<D>::kStages * Ring<D>::kBytes) + warp * (kScanGroup * kScan);
   long long* s_base = reinterpret_cast<long long*>(s_raw + kWarps * (Ring<D>::kStages * Ring<D>::kBytes +
                                                                      kScanGroup * kScan * (int)sizeof(Listed)));  // [S + 1]
+  // sequences as read for the numbering: length, first token, queries, tiles per row tile
+  int4* s_seq = p.S <= kSeqCache ? reinterpret_cast<int4*>(s_base + ((p.S + 2) & ~1)) : nullptr;
   grid_dep_wait();
   grid_dep_launch_next();
 
@@ -709,7 +738,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
     long long x = 0;
     if (s < p.S) {
       const SeqInfo q = seq_info(p, s);
-      x = (long long)tiles_per_row_tile(p, q, R) * row_tiles(p, q, R) * p.Hkv;
+      const int per_rt = tiles_per_row_tile(p, q, R);
+      x = (long long)per_rt * row_tiles(p, q, R) * p.Hkv;
+      if (s_seq) s_seq[s] = make_int4(q.len, q.tok0, q.nq, per_rt);
       if (q.bad && blockIdx.x == 0) record_failure(p.err, nullptr, SEP_ERR_INDEX);
     }
     long long inc = x;
@@ -733,9 +764,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
   if (blockIdx.x == 0)
     for (int s = tid; s <= p.S; s += kWarps * 32) p.base[s] = s_base[s];
   const long long total = carry;
-  const int gw = blockIdx.x * kWarps + warp;
+  const int gw = warp * gridDim.x + blockIdx.x;
   // padding queries (sequences without a key) have no tile: their rows are written here
   for (int s = gw; s < p.S; s += p.nwarps) {
+    if (s_base[s + 1] > s_base[s]) continue;
     const SeqInfo q = seq_info(p, s);
     if (q.nq > 0 && q.len == 0) {
       const long long at = (long long)q.tok0 * p.Hq, cnt = (long long)q.nq * p.Hq;
@@ -745,9 +777,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
         for (long long e = lane; e < cnt; e += 32) p.lse[at + e] = -INFINITY;
     }
   }
-  const long long per = quotient(total + p.nwarps - 1, p.nwarps);
-  long long x = (long long)gw * per;
-  const long long x_end = min(total, x + per);
+  const Split split(total, p.nwarps);
+  long long x = split.start(gw);
+  const long long x_end = split.start(gw + 1);
   if (x >= x_end) return;
 
   // ---- sequence of tile x: last s with s_base[s] <= x (sequences without tiles share a start)
@@ -763,12 +795,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
   bool first_segment = true;
   while (x < x_end) {
     while (s_base[seq + 1] <= x) ++seq;
-    const SeqInfo q = seq_info(p, seq);
-    const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+    SeqInfo q;
+    int per_rt;
+    if (s_seq) {
+      const int4 y = s_seq[seq];
+      q = SeqInfo{y.x, y.y, y.z, y.x - y.z, false};
+      per_rt = y.w;
+    } else {
+      q = seq_info(p, seq);
+      per_rt = tiles_per_row_tile(p, q, R);
+    }
+    const int nrt = row_tiles(p, q, R);
     const long long unit = quotient(x - s_base[seq], per_rt);
     const int ta = (int)((x - s_base[seq]) - unit * per_rt);
     const int tb = (int)min((long long)per_rt, ta + (x_end - x));
-    const int h = (int)quotient(unit, nrt), rt = (int)(unit - (long long)h * nrt);
+    const int h = nrt == 1 ? (int)unit : (int)quotient(unit, nrt), rt = (int)(unit - (long long)h * nrt);
     const RowTile w = row_tile(p, q, rt, R);
     const int da = max(ta, w.ns) - w.ns, db = min(tb - w.ns, w.nd);
     const int c0 = w.w0 + da * kDense, c1 = min(w.kend, w.w0 + db * kDense);
@@ -782,6 +823,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn_kernel(con
     if (da < db) {
       const int lo = q.lead + rt * R / p.G;
       const int hi = q.lead + min(q.nq - 1, (rt * R + R - 1) / p.G);
+      window_scales(p, win, c0, c1);
       window_keys<D, NT>(p, r, win, seq, h, q.len, lo, hi, c0, c1, ring, lane);
     }
     const bool whole = ta == 0 && tb == per_rt;
@@ -808,13 +850,13 @@ struct JoinShared {
 // Row `row` of a sequence and KV head, by the whole CTA; its row tile's tiles are t0 .. t1 - 1.
 template <int D, int NT>
 __device__ __forceinline__ void join_row(const PagedAttnParams& p, JoinShared<D>& sh, const SeqInfo& q, int h, int row,
-                                         long long t0, long long t1, long long per) {
+                                         long long t0, long long t1, const Split& split) {
   constexpr int R = 8 * NT, LPR = JoinShared<D>::LPR, GR = JoinShared<D>::GR;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lr = row % R, tok = q.tok0 + row / p.G, hq = h * p.G + row % p.G;
-  const int w0 = (int)quotient(t0, per), w1 = (int)quotient(t1 - 1, per), parts = w1 - w0 + 1;
+  const int w0 = split.owner(t0), w1 = split.owner(t1 - 1), parts = w1 - w0 + 1;
   if (parts == 1) return;
-  const int first_slot = t0 > (long long)w0 * per ? 1 : 0;
+  const int first_slot = t0 > split.start(w0) ? 1 : 0;
   auto part = [&](int i) -> const float* { return part_of<D, R>(p, w0 + i, i == 0 ? first_slot : 0); };
   // ---- maxima
   float mo = -INFINITY, m = -INFINITY;
@@ -888,15 +930,26 @@ __device__ __forceinline__ void join_row(const PagedAttnParams& p, JoinShared<D>
 // The same by one warp (many rows of few parts each).
 template <int D, int NT>
 __device__ __forceinline__ void join_row_warp(const PagedAttnParams& p, const SeqInfo& q, int h, int row, long long t0,
-                                              long long t1, long long per) {
+                                              long long t1, const Split& split) {
   constexpr int R = 8 * NT, F = D / 32;  // columns per lane
   const int lane = threadIdx.x & 31;
   const int lr = row % R, tok = q.tok0 + row / p.G, hq = h * p.G + row % p.G;
-  const int w0 = (int)quotient(t0, per), w1 = (int)quotient(t1 - 1, per), parts = w1 - w0 + 1;
+  const int w0 = split.owner(t0), w1 = split.owner(t1 - 1), parts = w1 - w0 + 1;
   if (parts == 1) return;
-  const int first_slot = t0 > (long long)w0 * per ? 1 : 0;
+  const int first_slot = t0 > split.start(w0) ? 1 : 0;
   auto part = [&](int i) -> const float* { return part_of<D, R>(p, w0 + i, i == 0 ? first_slot : 0); };
   auto stats = [&](int i) { return *reinterpret_cast<const float4*>(part(i) + (size_t)R * D + lr * 4); };
+  // the first parts' columns are requested with the statistics
+  constexpr int kAhead = 4;
+  auto columns = [&](int i) {
+    const float* a = part(i) + (size_t)lr * D + lane * F;
+    if (F == 4) return *reinterpret_cast<const float4*>(a);
+    const float2 v = *reinterpret_cast<const float2*>(a);
+    return make_float4(v.x, v.y, 0.f, 0.f);
+  };
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ahead[i] = i < parts ? columns(i) : make_float4(0.f, 0.f, 0.f, 0.f);
   float4 st = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);  // of part `lane`
   if (lane < parts) st = stats(lane);
   float mo = st.x, m = st.y;
@@ -918,23 +971,23 @@ __device__ __forceinline__ void join_row_warp(const PagedAttnParams& p, const Se
     if (b > 0) st = b + lane < parts ? stats(b + lane) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
     const float f = ex2(st.x - mor);
     l += b + lane < parts ? st.z * ex2(st.y - mr) : 0.f;
-    const int n = min(32, parts - b);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* a = part(b + i) + (size_t)lr * D + lane * F;
-      const float fi = __shfl_sync(0xffffffffu, f, i);
+    auto add = [&](const float4& v, float fi) {
+      acc[0] = fmaf(v.x, fi, acc[0]);
+      acc[1] = fmaf(v.y, fi, acc[1]);
       if (F == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(a);
-        acc[0] = fmaf(v.x, fi, acc[0]);
-        acc[1] = fmaf(v.y, fi, acc[1]);
         acc[F - 2] = fmaf(v.z, fi, acc[F - 2]);
         acc[F - 1] = fmaf(v.w, fi, acc[F - 1]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(a);
-        acc[0] = fmaf(v.x, fi, acc[0]);
-        acc[1] = fmaf(v.y, fi, acc[1]);
       }
+    };
+    const int n = min(32, parts - b);
+    int i = 0;
+    if (b == 0) {
+#pragma unroll
+      for (; i < kAhead; ++i)
+        if (i < n) add(ahead[i], __shfl_sync(0xffffffffu, f, i));
     }
+#pragma unroll 4
+    for (; i < n; ++i) add(columns(b + i), __shfl_sync(0xffffffffu, f, i));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -969,7 +1022,7 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_const
   const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
   const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
   const long long t0 = base + ((long long)h * nrt + row / R) * per_rt;
-  join_row_warp<D, NT>(p, q, h, row, t0, t0 + per_rt, quotient(total + p.nwarps - 1, p.nwarps));
+  join_row_warp<D, NT>(p, q, h, row, t0, t0 + per_rt, Split(total, p.nwarps));
 }
 
 // One CTA per (query token, query head); where chunks are present (and most tokens belong to them), one
@@ -986,9 +1039,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     if (parts > 1)
       for (int x = blockIdx.x * (kJoinThreads / 32) + tid / 32; x < items * kRowsPerItem; x += gridDim.x * (kJoinThreads / 32))
         chunk_join_row<D>(p, x / kRowsPerItem, x % kRowsPerItem, parts, tid & 31);
-    const long long total = p.base[p.S], per = quotient(total + p.nwarps - 1, p.nwarps);
-    const long long x = (blockIdx.x + 1ll) * per;
-    if (x >= total) return;
+    const long long total = p.base[p.S];
+    const Split split(total, p.nwarps);
+    const long long x = split.start(blockIdx.x + 1);
+    if (x >= total || x == split.start(blockIdx.x)) return;
     int lo = 0, hi = p.S;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -998,10 +1052,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const SeqInfo q = seq_info(p, lo);
     const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
     const long long unit = quotient(x - p.base[lo], per_rt), t0 = p.base[lo] + unit * per_rt;
-    if (t0 == x || quotient(t0, per) != blockIdx.x) return;
+    if (t0 == x || split.owner(t0) != (int)blockIdx.x) return;
     const int h = (int)quotient(unit, nrt), rt = (int)(unit - (long long)h * nrt);
     for (int row = rt * R; row < min(rt * R + R, q.nq * p.G); ++row) {
-      join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, per);
+      join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, split);
       __syncthreads();
     }
     return;
@@ -1020,12 +1074,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
   const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
   const long long t0 = p.base[seq] + ((long long)h * nrt + row / R) * per_rt;
-  join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, (p.base[p.S] + p.nwarps - 1) / p.nwarps);
+  join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, Split(p.base[p.S], p.nwarps));
 }
 
 template <int D, int NT>
 cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
-  const size_t smem = (size_t)(p.S + 1) * sizeof(long long) +
+  const size_t smem = (size_t)(p.S + 2) * sizeof(long long) + (p.S <= kSeqCache ? p.S * sizeof(int4) : 0) +
                       (size_t)kWarps * (kScanGroup * kScan * sizeof(Listed) + Ring<D>::kStages * Ring<D>::kBytes);
   static std::atomic<bool> set[64];
   int dev = 0;
