@@ -144,11 +144,9 @@ __device__ __forceinline__ void turn(const SepRope& r, Item it, const uint4& a, 
   widen8<T>(b, x + 4);
   if (it.e0 >= r.d_rot) return;
   if (PAIRED) {
-    // e0 and the row's pairs are multiples of 8; two pairs of the table per load
-    const float4* c4 = reinterpret_cast<const float4*>(cs + it.e0);
 #pragma unroll
     for (int z = 0; z < 4; ++z) {
-      const float4 c = c4[z];
+      const float4 c = table_pairs<8>(cs, r.d_rot >> 1, it.e0 >> 3, z);
       const float2 x1 = x[z], x2 = x[4 + z];
       x[z] = make_float2(__fmaf_rn(x1.x, c.x, -__fmul_rn(x2.x, c.y)), __fmaf_rn(x1.y, c.z, -__fmul_rn(x2.y, c.w)));
       x[4 + z] = make_float2(__fmaf_rn(x2.x, c.x, __fmul_rn(x1.x, c.y)), __fmaf_rn(x2.y, c.z, __fmul_rn(x1.y, c.w)));
@@ -304,7 +302,7 @@ __global__ void __launch_bounds__(512) paged_append_page_kernel(const __grid_con
   for (int c = 0; c < 2; ++c) ka[c] = kb[c] = va[c] = vb[c] = make_uint4(0u, 0u, 0u, 0u);
   load(h_begin + team);
   if (tt < 2) s_top[0][team][tt] = 0;
-  angle_table(s_cs, u.nrow, h, st.rope.freq, st.rope.magnitude, st.rope.magnitude, tid, nthr,
+  angle_table<PAIRED ? 8 : 1>(s_cs, u.nrow, h, st.rope.freq, st.rope.magnitude, st.rope.magnitude, tid, nthr,
               [&](int r) { return (double)(u.r0 + r); });
   if (blockIdx.y == 0)
     for (int r = tid; r < u.nrow; r += nthr)
@@ -441,7 +439,7 @@ __global__ void __launch_bounds__(128) paged_append_rows_kernel(const __grid_con
       vb = *reinterpret_cast<const uint4*>(v + 16 * j + 8);
     }
     __syncthreads();  // the last round's table has been read
-    angle_table(s_cs, min(ROWS, u.nrow - base), h, st.rope.freq, st.rope.magnitude, st.rope.magnitude, tid, 128,
+    angle_table<PAIRED ? 8 : 1>(s_cs, min(ROWS, u.nrow - base), h, st.rope.freq, st.rope.magnitude, st.rope.magnitude, tid, 128,
                 [&](int r) { return (double)(u.r0 + base + r); });
     __syncthreads();
     if (live) {

@@ -60,35 +60,38 @@ struct Step {
   static constexpr bool kOne = INTER && VEC == 1;                 // pair by pair
   static constexpr bool kTwo = !INTER || kOne;                    // two groups
   static constexpr int kWide = INTER && VEC > 1 ? VEC / 2 : VEC;  // pairs of a step
-  int at, at2, pair;  // first elements of the groups, first pair
-  __device__ __forceinline__ Step(const RopeParams& p, int u) {
-    pair = u * kWide;
-    at = INTER ? 2 * pair : pair;
-    at2 = kOne ? at + 1 : pair + (p.d_rot >> 1);
+  int at, at2, u, h;  // first elements of the groups, step, pairs of a row
+  __device__ __forceinline__ Step(const RopeParams& p, int step) : u(step), h(p.d_rot >> 1) {
+    at = (INTER ? 2 : 1) * kWide * u;
+    at2 = kOne ? at + 1 : at + h;
   }
   __device__ __forceinline__ void load(const T* x, Gr& a, Gr& b) const {
     a = *reinterpret_cast<const Gr*>(x + at);
     if (kTwo) b = *reinterpret_cast<const Gr*>(x + at2);
   }
   __device__ __forceinline__ void turn_store(T* y, Gr a, Gr b, const float2* cs) const {
-    if (!kTwo) {
-#pragma unroll
-      for (int z = 0; z + 1 < VEC; z += 2) {
-        const float2 c = cs[pair + (z >> 1)];
-        const float x1 = to_float(a.v[z]), x2 = to_float(a.v[z + 1]);
-        a.v[z] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
-        a.v[z + 1] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
-      }
+    auto turn = [](T& p1, T& p2, float c, float s) {
+      const float x1 = to_float(p1), x2 = to_float(p2);
+      p1 = from_float<T>(__fmaf_rn(x1, c, -__fmul_rn(x2, s)));
+      p2 = from_float<T>(__fmaf_rn(x2, c, __fmul_rn(x1, s)));
+    };
+    if (kWide == 1) {
+      const float2 c = cs[u];
+      turn(a.v[0], b.v[0], c.x, c.y);
     } else {
 #pragma unroll
-      for (int z = 0; z < VEC; ++z) {
-        const float2 c = cs[pair + z];
-        const float x1 = to_float(a.v[z]), x2 = to_float(b.v[z]);
-        a.v[z] = from_float<T>(__fmaf_rn(x1, c.x, -__fmul_rn(x2, c.y)));
-        b.v[z] = from_float<T>(__fmaf_rn(x2, c.x, __fmul_rn(x1, c.y)));
+      for (int z = 0; z < kWide / 2; ++z) {
+        const float4 c = table_pairs<kWide>(cs, h, u, z);
+        if (kTwo) {
+          turn(a.v[(2 * z) % VEC], b.v[(2 * z) % VEC], c.x, c.y);
+          turn(a.v[(2 * z + 1) % VEC], b.v[(2 * z + 1) % VEC], c.z, c.w);
+        } else {
+          turn(a.v[(4 * z) % VEC], a.v[(4 * z + 1) % VEC], c.x, c.y);
+          turn(a.v[(4 * z + 2) % VEC], a.v[(4 * z + 3) % VEC], c.z, c.w);
+        }
       }
-      *reinterpret_cast<Gr*>(y + at2) = b;
     }
+    if (kTwo) *reinterpret_cast<Gr*>(y + at2) = b;
     *reinterpret_cast<Gr*>(y + at) = a;
   }
 };
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch_next();
-  angle_table(s_cs, nt, h, p.freq, p.magnitude, p.magnitude * p.sign, tid, kRopeThreads, [&](int r) {
+  angle_table<St::kWide>(s_cs, nt, h, p.freq, p.magnitude, p.magnitude * p.sign, tid, kRopeThreads, [&](int r) {
     return p.pos64 ? (double)static_cast<const long long*>(p.pos)[s_pos[r]]
                    : (double)static_cast<const int*>(p.pos)[s_pos[r]];
   });

@@ -19,8 +19,19 @@ __device__ __forceinline__ float2 turn_cos_sin(double pos, double turns) {
 }
 
 // The (cos, sin) table [rows][h] of positions pos_of(0) .. pos_of(rows - 1), by nthr threads: a thread
-// keeps one pair's frequency and goes down the rows. mc, ms: factors of cos and sin.
-template <typename PosOf>
+// keeps one pair's frequency and goes down the rows. mc, ms: factors of cos and sin. Lanes take W
+// consecutive pairs each, two per 16-byte load: the first two of every lane lie side by side in a row,
+// then the next two, so that neighbouring lanes read neighbouring banks (table_pairs).
+template <int W>
+__device__ __forceinline__ int table_slot(int pair, int h) {
+  return W == 1 ? pair : 2 * ((pair % W / 2) * (h / W) + pair / W) + (pair & 1);
+}
+// Pairs 2 z and 2 z + 1 of group u of a row: (cos, sin, cos, sin).
+template <int W>
+__device__ __forceinline__ float4 table_pairs(const float2* row, int h, int u, int z) {
+  return reinterpret_cast<const float4*>(row)[z * (h / W) + u];
+}
+template <int W, typename PosOf>
 __device__ __forceinline__ void angle_table(float2* cs, int rows, int h, const double* freq, float mc, float ms,
                                             int tid, int nthr, PosOf pos_of) {
   if (h == 0) return;
@@ -28,9 +39,10 @@ __device__ __forceinline__ void angle_table(float2* cs, int rows, int h, const d
   if (r0 >= per) return;
   for (int z = z0; z < h; z += nthr) {  // one round unless there are more pairs than threads
     const double turns = __dmul_rn(__ldg(freq + z), kInvTwoPi);
+    const int at = table_slot<W>(z, h);
     for (int r = r0; r < rows; r += per) {
       const float2 c = turn_cos_sin(pos_of(r), turns);
-      cs[r * h + z] = make_float2(c.x * mc, c.y * ms);
+      cs[r * h + at] = make_float2(c.x * mc, c.y * ms);
     }
   }
 }
