@@ -578,6 +578,10 @@ def _rope_side(name, t, lead, nd, dtype, y):
     if y is None:
         y = torch.empty_like(t, memory_format=_CONTIGUOUS)
         ys, yptr = y.stride(), y.data_ptr()
+    elif y is t:
+        ys, yptr = st, ptr
+        if 0 in st and any(n > 1 and x == 0 for n, x in zip(shape, st)):
+            raise SepError(f"out {name} is an expanded view: its rows share memory")
     else:
         _strided(y, (dtype,), f"out {name}", shape)
         ys = y.stride()
@@ -624,8 +628,11 @@ def _rope_call(fn, what, q, k, positions, rope, out):
         if yq is None:
             raise SepError("out must hold one tensor for each of q and k")
         if k is not None:
-            for what_else, x, y in (("the other one's input", yk, q), ("the other one's input", yq, k),
-                                    ("each other", yq, yk)):
+            # in place the three questions are one
+            pairs = (("each other", yq, yk),) if yq is q and yk is k else (
+                ("the other one's input", yk, q), ("the other one's input", yq, k),
+                ("each other", yq, yk))
+            for what_else, x, y in pairs:
                 if isinstance(x, torch.Tensor) and isinstance(y, torch.Tensor) and \
                         x.dim() == nd and y.dim() == nd and _overlap(x, y):
                     raise SepError(f"the outputs of q and k overlap {what_else}")
@@ -651,6 +658,8 @@ def _rope_call(fn, what, q, k, positions, rope, out):
 
 def _extent(t):
     """First and last byte address (exclusive) of a tensor with non-negative strides."""
+    if t.is_contiguous():
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
     last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
@@ -755,15 +764,23 @@ class SepPagedCache:
                              (r.freq.data_ptr(), r.d_rot, r.interleaved, r.magnitude)))
 
     def _state(self):
-        """Checks the cache's own tensors (a caller may put its own buffers in their place)."""
+        """Checks the cache's own tensors where a caller has put its own buffers in their place."""
+        seen = self._seen
+        if (seen is not None and self.k_pages is seen[0] and self.v_pages is seen[1] and
+                self.k_scale is seen[2] and self.v_scale is seen[3] and self.flags is seen[4]):
+            return
         pages, per_head = (self.num_pages, self.Hkv, self.page, self.d), (self.num_pages, self.Hkv)
         for name, t, dtype, shape in (("k_pages", self.k_pages, torch.float8_e4m3fn, pages),
                                       ("v_pages", self.v_pages, torch.float8_e4m3fn, pages),
                                       ("k_scale", self.k_scale, torch.float32, per_head),
                                       ("v_scale", self.v_scale, torch.float32, per_head),
                                       ("flags", self.flags, torch.uint8, pages[::2])):
-            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+            if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or \
+                    not t.is_contiguous() or not t.is_cuda:
                 _cuda(t, dtype, name, shape)
+        self._seen = (self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.flags)
+
+    _seen = None
 
     @staticmethod
     def _plan(page_table, seq_lens, indptr):
@@ -771,11 +788,15 @@ class SepPagedCache:
         S, max_pages = _dims(page_table, 2, "page_table")
         if S < 1 or max_pages < 1:
             raise SepError("page_table needs at least one sequence and one page")
-        for name, t, shape in (("page_table", page_table, (S, max_pages)),
-                               ("seq_lens", seq_lens, (S,)), ("indptr", indptr, (S + 1,))):
-            if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not torch.int32
-                    or not t.is_contiguous() or not t.is_cuda):
-                _cuda(t, torch.int32, name, shape)
+        i32, tensor = torch.int32, torch.Tensor
+        if page_table.dtype is not i32 or not page_table.is_contiguous() or not page_table.is_cuda:
+            _cuda(page_table, i32, "page_table")
+        if (not isinstance(seq_lens, tensor) or seq_lens.shape != (S,) or seq_lens.dtype is not i32
+                or not seq_lens.is_contiguous() or not seq_lens.is_cuda):
+            _cuda(seq_lens, i32, "seq_lens", (S,))
+        if (not isinstance(indptr, tensor) or indptr.shape != (S + 1,) or indptr.dtype is not i32
+                or not indptr.is_contiguous() or not indptr.is_cuda):
+            _cuda(indptr, i32, "indptr", (S + 1,))
         return S, max_pages
 
     @staticmethod
