@@ -228,8 +228,9 @@ cudaError_t launch_rope(const SepRope& r, int dtype, int B, int L, int d, const 
   p.copy_rest = !inplace;
   p.magnitude = r.magnitude;
   p.sign = sign;
-  // one wave of CTAs while that gives each up to kRopeMaxTokens tokens
-  p.tokens = (int)std::min<long long>(kRopeMaxTokens, (p.ntok + 148 * kRopeCtas - 1) / (148 * kRopeCtas));
+  // one wave of CTAs while that gives each up to kRopeMaxTokens tokens, their table within 40 KB
+  const int most = std::min(kRopeMaxTokens, 40 * 1024 / (int)(p.d_rot / 2 * sizeof(float2)));
+  p.tokens = (int)std::min<long long>(most, (p.ntok + 148 * kRopeCtas - 1) / (148 * kRopeCtas));
   if (dtype == SEP_DTYPE_BF16) return launch_rope_t<__nv_bfloat16>(p, vec, stream);
   if (dtype == SEP_DTYPE_F16) return launch_rope_t<__half>(p, vec, stream);
   return launch_rope_t<float>(p, vec, stream);

@@ -469,7 +469,10 @@ class SepRope:
     magnitude: float
 
     def _packed(self):
-        """The C struct SepRope."""
+        """The C struct SepRope (the library reads d_rot / 2 angles)."""
+        if (self.freq.numel() * 2 != self.d_rot or self.freq.dtype is not torch.float64
+                or not self.freq.is_contiguous()):
+            raise SepError(f"rope.freq must be {self.d_rot // 2} contiguous float64 values")
         return _ROPE.pack(self.freq.data_ptr(), self.d_rot, self.interleaved, self.magnitude)
 
 
@@ -757,6 +760,8 @@ class SepPagedCache:
     def _packed(self):
         """The C struct SepPagedState."""
         r = self.rope
+        if r is not None:
+            r._packed()
         return _PAGED.pack(self.num_pages, self.Hkv, self.d, self.page, self.k_pages.data_ptr(),
                            self.v_pages.data_ptr(), self.k_scale.data_ptr(),
                            self.v_scale.data_ptr(), self.flags.data_ptr(),

@@ -292,6 +292,7 @@ ATTN = [
     ((1400, 50, 0, 7), (100, 80, 60, 50), 3, 3, 64, 16, "bfloat16", 1, 1),  # queries before position 0, no key
     ((300,) * 9, (40,) * 9, 16, 16, 64, 64, "float16", 0, None),
     ((300,) * 10, (40,) * 10, 16, 16, 64, 64, "float16", 1, 40),  # more items than SMs
+    ((300, 64, 5000), (1, 1, 1), 40, 1, 64, 16, "bfloat16", 0, None),  # single tokens of a wide group
     ((6000, 200), (40, 3), 1, 1, 128, 64, "bfloat16", 0, None),   # one item, cut along its keys
     ((6000, 200), (40, 3), 2, 1, 64, 32, "bfloat16", 4, 200),
 ]

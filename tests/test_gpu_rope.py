@@ -52,6 +52,8 @@ CASES = [
     ("bfloat16", (2, 9), 3, 1, 66, 10, True, None),                               # unaligned rows
     ("float32", (41,), 2, 1, 6, 2, False, None),
     ("bfloat16", (1, 5000), 4, 1, 256, 256, False, None),                         # many tokens per CTA
+    ("bfloat16", (40000,), 1, 1, 512, 512, False, None),                          # the largest table
+    ("float32", (3, 900), 2, 2, 320, 316, True, None),
 ]
 
 

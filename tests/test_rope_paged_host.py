@@ -99,6 +99,9 @@ def test_rope_binding_refusals():
             call(q, q, pos, _rope(128))
         with pytest.raises(S.SepError, match="tokens, heads, d"):
             call(q[0, 0], None, pos, _rope())
+    for bad in (torch.zeros(31, dtype=torch.float64), torch.zeros(32), torch.zeros(64, dtype=torch.float64)[::2]):
+        with pytest.raises(S.SepError, match="32 contiguous float64"):
+            S.SepRope(bad, 64, False, 1.0)._packed()
 
 
 def test_address_ranges_of_views():
