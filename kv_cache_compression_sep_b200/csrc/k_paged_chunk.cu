@@ -561,10 +561,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
           return p.bf16 ? make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u))
                         : __half22float2(*reinterpret_cast<const __half2*>(&v));
         };
-#pragma unroll 4
+        uint4 qv[D / 8];  // (requested at once)
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          qv[c] = live ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t vs[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float2 f = pair(vs[y]);
@@ -575,10 +578,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
         const int sh = max(-110, min(110, 13 - ex));
         const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t vs[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
           uint32_t o[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
