@@ -61,7 +61,7 @@ struct __align__(16) TileDesc {
 };
 struct ChunkBar {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2][2], p_ready[2][2], pv_done[2];
+  uint64_t q_full[2], s_full[2][2], p_ready[2][2], pv_done[2], o_done[2];
   uint64_t conv, drain;
   TileDesc desc[4];
   KeyPut keys[2][128];
@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
       mbar_init(&bar->p_ready[s][0], 128);
       mbar_init(&bar->p_ready[s][1], 128);
       mbar_init(&bar->pv_done[s], 1);
+      mbar_init(&bar->o_done[s], 1);
     }
     mbar_init(&bar->conv, 128);
     mbar_init(&bar->drain, 1);
@@ -522,6 +523,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
               mma_ts(tmem + C::COL_O + w * D, aP + kk * 8, sdesc_join(vlo + kk * (2048 >> 4), kDescHi), idO,
                      (!first || kk > 0) ? 1u : 0u);
             tc_commit(&bar->pv_done[w]);
+            if (last && z >= 2) tc_commit(&bar->o_done[w]);
             if (z == 3) tc_commit(&bar->v_empty[st]);
             if (w == 1) first = false;
             if (!last) {
@@ -702,9 +704,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         }
         if (!ok) break;
         // ---- output
-        // (the last P V but one first: a parity names the phase before the current one only)
-        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], 0, p.err, abort_flag)))) break;
-        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->pv_done[w], 1, p.err, abort_flag)))) break;
+        // (pv_done has two phases that may both be over or under way here, which a parity cannot tell apart:
+        // o_done has one per item)
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar->o_done[w], slot & 1, p.err, abort_flag)))) break;
         tc_fence_after();
         if (row_nan) l_run = __uint_as_float(0x7fffffffu);
         const bool none = m_run == -INFINITY && !row_nan;

@@ -561,6 +561,28 @@ def test_decode_in_a_graph_two_streams_shared_prefix(S):
         assert torch.equal(st["cache"].k_pages.view(torch.uint8), cache.k_pages.view(torch.uint8))
 
 
+def test_chunks_beside_each_other(S):
+    """Chunks of many short items on two streams at once, where warps of one call are held up by the
+    other's at any point: every wait ends, and the results are those of a call alone."""
+    import torch
+    lens, counts = [130, 70, 260, 40] * 6, [130, 70, 130, 40] * 6
+    pair = filled(S, len(lens), lens, 8, 64, 64, seed=5)
+    q = draw(9, sum(counts), 16, 64, torch.bfloat16)
+    args = (q, ints(pair.table.tolist()), ints(lens), ints(np.concatenate([[0], np.cumsum(counts)]).tolist()))
+    want, want_lse = pair.cache.seppaged_attn(*args, a=2, n=48)
+    torch.cuda.synchronize()
+    got = []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(40):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(pair.cache.seppaged_attn(*args, a=2, n=48))
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    for o, lse in got:
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
 def test_prompt_in_chunks_equals_the_separator_attention(S):
     """A prompt rotated and appended chunk by chunk, each chunk attending to its past, against
     sep_attn_fwd over the same (stored) keys and values in bf16: the e4m3 numbers times a power of two are
