@@ -120,15 +120,6 @@ struct Ring {
     return (uint32_t)(row * D + ((piece ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4));
   }
 };
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
-  // a size of 0 reads nothing and fills with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -1035,10 +1026,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   grid_dep_launch_next();
   const int tid = threadIdx.x;
   if (p.chunks) {
-    const int parts = p.chunk_plan[1], items = p.chunk_plan[0];
-    if (parts > 1)
-      for (int x = blockIdx.x * (kJoinThreads / 32) + tid / 32; x < items * kRowsPerItem; x += gridDim.x * (kJoinThreads / 32))
-        chunk_join_row<D>(p, x / kRowsPerItem, x % kRowsPerItem, parts, tid & 31);
+    // a CTA per 32 rows of an item that was cut
+    constexpr int PER = kRowsPerItem / 32;
+    for (int x = blockIdx.x; x < kChunkCtas * PER; x += gridDim.x) {
+      const int c = x / PER, parts = p.chunk_plan[2 * c + 1];
+      if (parts == 0) continue;
+      const Item it = chunk_item(p, p.chunk_plan + kPlanInts, p.chunk_plan[2 * c], 0, 0);
+      for (int i = tid / 32; i < D / 8; i += kJoinThreads / 32)
+        chunk_join_rows<D>(p, it, c, parts, x % PER * 32 + i % 4 * 8, i / 4 * 32, tid & 31);
+    }
     const long long total = p.base[p.S];
     const Split split(total, p.nwarps);
     const long long x = split.start(blockIdx.x + 1);
@@ -1106,7 +1102,7 @@ cudaError_t launch_paged_attn_t(PagedAttnParams p, cudaStream_t stream) {
 
 }  // namespace
 
-// Workspace: [S + 1] tile numbers, [S + 3] plan of the chunks, two parts per warp (16 rows at most), parts of
+// Workspace: [S + 1] tile numbers, plan of the chunks, two parts per warp (16 rows at most), parts of
 // the chunks.
 namespace {
 struct PagedWs {
@@ -1116,9 +1112,9 @@ PagedWs paged_ws(int S, int d) {
   PagedWs w;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w.plan = up((size_t)(S + 1) * sizeof(long long));
-  w.part = w.plan + up((size_t)(S + 3) * sizeof(int));
+  w.part = w.plan + up((size_t)(S + 1 + kPlanInts) * sizeof(int));
   w.chunk = w.part + up((size_t)kMaxWarps * 2 * 16 * (d + 4) * sizeof(float));
-  w.total = w.chunk + (size_t)kChunkCtas * kRowsPerItem * (d + 4) * sizeof(float);
+  w.total = w.chunk + (size_t)kChunkParts * kRowsPerItem * (d + 4) * sizeof(float);
   return w;
 }
 }  // namespace

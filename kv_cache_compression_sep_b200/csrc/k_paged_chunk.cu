@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "sep_common.cuh"
 #include "sep_launch.h"
@@ -71,6 +72,8 @@ struct ChunkBar {
   int ex_k[4], ex_v[4], nan[4];
   int red[4], part4[4], any_far[2][4], hole[2][4];
   int part[16];
+  long long sum[16], sum0[16];
+  int cut_item[2], cut_step[2], cut_last;  // ends of the CTA's run; last CTA with a part of the item at its end
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
   grid_dep_wait();
   grid_dep_launch_next();
   // ---- first item of every sequence
-  int carry = 0, steps = 0;
+  int carry = 0;
   __syncthreads();
   for (int s0 = 0; s0 < p.S; s0 += C::THREADS) {
     const int s = s0 + tid;
@@ -185,7 +188,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     if (s < p.S) {
       const SeqInfo q = seq_info(p, s);
       x = chunk_items(p, q);
-      if (x > 0) steps = max(steps, chunk_steps(p, q));
     }
     int inc = x;
 #pragma unroll
@@ -204,21 +206,100 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     __syncthreads();
   }
   if (tid == 0) base[p.S] = carry;
-  steps = __reduce_max_sync(0xffffffffu, steps);
-  if (lane == 0) bar->part[warp] = steps;
   __syncthreads();
-  for (int w = 0; w < C::THREADS / 32; ++w) steps = max(steps, bar->part[w]);
-  // Few items are cut along their keys so that every SM has a part, of four steps at least.
-  const int parts = carry == 0 ? 1 : max(1, min(kChunkCtas / carry, steps / 4));
-  const int nitems = carry * parts;
-  if (blockIdx.x == 0) {
-    for (int s = tid; s <= p.S; s += C::THREADS) p.chunk_plan[2 + s] = base[s];
-    if (tid == 0) {
-      p.chunk_plan[0] = carry;
-      p.chunk_plan[1] = parts;
+  // ---- this CTA's items first + i stride, from step step0 of the first to step1 of the last
+  const int cta = blockIdx.x, tiles = carry / p.Hkv;
+  auto units_of = [&](int f) { return chunk_item(p, base, f * p.Hkv, 0, 0).steps + kStartUnits; };
+  long long total = 0, load0 = 0;  // units; those of CTA 0 if it takes every 148th item whole
+  int units0 = 0;
+  for (int f = tid; f < tiles; f += C::THREADS) {
+    const int v = units_of(f);
+    if (f == tid) units0 = v;
+    total += (long long)v * p.Hkv;
+    load0 += (long long)v * (((f + 1) * p.Hkv + kChunkCtas - 1) / kChunkCtas - (f * p.Hkv + kChunkCtas - 1) / kChunkCtas);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    load0 += __shfl_xor_sync(0xffffffffu, load0, o);
+  }
+  if (lane == 0) {
+    bar->sum[warp] = total;
+    bar->sum0[warp] = load0;
+  }
+  __syncthreads();
+  total = load0 = 0;
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    total += bar->sum[w];
+    load0 += bar->sum0[w];
+  }
+  const bool cut = (load0 - kCutUnits) * kChunkCtas > total;
+  int first = cta, stride = kChunkCtas, nitems = carry > cta ? (carry - cta - 1) / kChunkCtas + 1 : 0;
+  int step0 = 0, step1 = INT_MAX, parts = 0;
+  if (cut) {
+    const int ctas = (int)min((long long)kChunkCtas, max(1ll, total / (kStartUnits + 4)));
+    nitems = 0;
+    if (cta < ctas) {
+      if (tid == 0) {
+        bar->cut_item[1] = carry;  // (the line's end)
+        bar->cut_step[1] = 0;
+      }
+      long long before = 0;
+      for (int f0 = 0; f0 < tiles; f0 += C::THREADS) {
+        const int f = f0 + tid, v = f >= tiles ? 0 : f0 == 0 ? units0 : units_of(f);
+        const long long mine = (long long)v * p.Hkv;
+        long long at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += y;
+        }
+        __syncthreads();
+        if (lane == 31) bar->sum[warp] = at;
+        __syncthreads();
+        at += before - mine;
+        for (int w = 0; w < C::THREADS / 32; ++w) {
+          if (w < warp) at += bar->sum[w];
+          before += bar->sum[w];
+        }
+        for (int e = 0; e < 2; ++e) {
+          const long long b = (cta + e) * total / ctas - at;
+          if (b < 0 || b >= mine) continue;
+          const int h = (int)(b / v), steps = v - kStartUnits;
+          int item = f * p.Hkv + h, s = (int)(b - (long long)h * v) - kStartUnits;
+          if (s < kSnap) {
+            s = 0;
+          } else if (s > steps - kSnap) {
+            s = 0;
+            ++item;
+          }
+          bar->cut_item[e] = item;
+          bar->cut_step[e] = s;
+          // the last boundary at most `steps - kSnap` steps into the item
+          if (e == 1) bar->cut_last = (int)(((at + (long long)h * v + v - kSnap + 1) * ctas - 1) / total);
+        }
+      }
+      __syncthreads();
+      first = bar->cut_item[0];
+      step0 = bar->cut_step[0];
+      step1 = bar->cut_step[1];
+      stride = 1;
+      nitems = bar->cut_item[1] - first + (step1 > 0);
+      if (first == bar->cut_item[1] && step0 == step1) nitems = 0;
+      if (step1 > 0 && nitems > 0 && (nitems > 1 || step0 == 0)) parts = bar->cut_last - cta + 1;
+      if (step1 == 0) step1 = INT_MAX;
     }
   }
-  if ((int)blockIdx.x >= nitems) return;  // no tensor memory was taken
+  if (cta == 0)
+    for (int s = tid; s <= p.S; s += C::THREADS) p.chunk_plan[kPlanInts + s] = base[s];
+  if (tid == 0) {
+    p.chunk_plan[2 * cta] = first + nitems - 1;
+    p.chunk_plan[2 * cta + 1] = parts;
+  }
+  if (nitems == 0) return;  // no tensor memory was taken
+  auto item_at = [&](int x) {
+    return chunk_item(p, base, first + x * stride, x == 0 ? step0 : 0, x == nitems - 1 ? step1 : INT_MAX);
+  };
   if (warp == 12) {
     tmem_alloc(&bar->tmem_base, 512);
     tmem_relinquish();
@@ -242,8 +323,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
       return r;
     };
     int g = 0, slot = 0;
-    for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
-      const Item it = chunk_item(p, base, x, parts);
+    for (int x = 0; ok && x < nitems; ++x, slot = (slot + 1) & 3) {
+      const Item it = item_at(x);
       const int32_t* table = p.table + (long long)it.seq * p.max_pages;
       // ---- largest scales of the item's pages
       const int npages = (it.kend + (1 << p.log_page) - 1) >> p.log_page;
@@ -499,7 +580,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         }
         tc_commit(&bar->s_full[w][u & 1]);
       };
-      for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, ++item) {
+      for (; ok && item < nitems; ++item) {
         if (!(ok = wait_bar(&bar->q_full[0], item & 1, p.err, abort_flag))) break;
         if (!(ok = wait_bar(&bar->q_full[1], item & 1, p.err, abort_flag))) break;
         if (!(ok = wait_bar(&bar->k_full[g % NST], (g / NST) & 1, p.err, abort_flag))) break;
@@ -547,29 +628,45 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
     const int w = warp >> 2, row = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::COL_S + w * 128, tO = tmem + lane_off + C::COL_O + w * D;
+    // 16-byte pieces of the warp's own rows in the Q tile
+    constexpr int CH = D / 8;
+    auto piece_of = [&](int row, int c) {
+      return reinterpret_cast<uint4*>(sQ + w * C::TILE + (c >> 3) * C::BOX + sw128_offset(row, c & 7));
+    };
     bool ok = true;
     int g = 0, slot = 0;
-    for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, slot = (slot + 1) & 3) {
-      const Item it = chunk_item(p, base, x, parts);
+    for (int x = 0; ok && x < nitems; ++x, slot = (slot + 1) & 3) {
+      const Item it = item_at(x);
       const int r = it.r0 + w * 128 + row;
       const bool live = r < it.rows;
       const int tok = live ? r / p.G : 0, hq = it.h * p.G + (live ? r - tok * p.G : 0);
       const int pos = live ? it.q.lead + tok : -1;
       {
         // ---- the row of Q as fp16, its largest magnitude in [2^13, 2^14)
-        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (long long)(it.q.tok0 + tok) * p.q_tok + (long long)hq * p.q_head;
+        // The warp fetches its rows as wholes into their place in the tile; then each lane turns its own.
+        // (Short loops: this code runs once per item and comes from far away. Unrolled, with the row in
+        // registers, it took 10 us.)
+        const uint16_t* q = static_cast<const uint16_t*>(p.q);
+        const long long at = live ? (long long)(it.q.tok0 + tok) * p.q_tok + (long long)hq * p.q_head : LLONG_MIN;
+#pragma unroll 4
+        for (int c = 0; c < CH; ++c) {
+          const long long o = __shfl_sync(0xffffffffu, at, c * (32 / CH) + lane / CH);
+          const bool there = o != LLONG_MIN;
+          copy16(smem_u32(piece_of((row & ~31) + c * (32 / CH) + lane / CH, lane % CH)),
+                 reinterpret_cast<const uint8_t*>(q + (there ? o + lane % CH * 8 : 0)), there);
+        }
+        copy_commit();
+        copy_wait<0>();
+        __syncwarp();
         float top = 0.f;
         auto pair = [&](uint32_t v) {
           return p.bf16 ? make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u))
                         : __half22float2(*reinterpret_cast<const __half2*>(&v));
         };
-        uint4 qv[D / 8];  // (requested at once)
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          qv[c] = live ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t vs[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+#pragma unroll 2
+        for (int c = 0; c < CH; ++c) {
+          const uint4 v = *piece_of(row, c);
+          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float2 f = pair(vs[y]);
@@ -580,17 +677,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
         const int sh = max(-110, min(110, 13 - ex));
         const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t vs[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+#pragma unroll 2
+        for (int c = 0; c < CH; ++c) {
+          const uint4 v = *piece_of(row, c);
+          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float2 f = pair(vs[y]);
             o[y] = pack_half2(f.x * up, f.y * up);
           }
-          *reinterpret_cast<uint4*>(sQ + w * C::TILE + (c >> 3) * C::BOX + sw128_offset(row, c & 7)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          *piece_of(row, c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bar->q_full[w]);
@@ -712,8 +809,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
         const bool none = m_run == -INFINITY && !row_nan;
         const float vs = __uint_as_float((uint32_t)bar->ex_v[slot] << 23);
         const float f = none ? 0.f : vs / l_run;
-        if (parts > 1) {  // this part's own result, for the join
-          float* po = chunk_part_of<D>(p, x);
+        const bool goes_on = x == 0 && step0 > 0;
+        if (goes_on || (x == nitems - 1 && step1 != INT_MAX)) {  // this part's own result, for the join
+          float* po = chunk_part_of<D>(p, 2 * cta + !goes_on);
           const int pr = w * 128 + row;
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
@@ -723,7 +821,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
             if (live) {
 #pragma unroll
               for (int y = 0; y < 8; ++y)
-                *reinterpret_cast<float4*>(po + (size_t)pr * D + cc * 32 + 4 * y) =
+                *reinterpret_cast<float4*>(po + ((cc * 8 + y) * kRowsPerItem + pr) * 4) =
                     none ? make_float4(0.f, 0.f, 0.f, 0.f)
                          : make_float4(__uint_as_float(ov[4 * y]) * f, __uint_as_float(ov[4 * y + 1]) * f,
                                        __uint_as_float(ov[4 * y + 2]) * f, __uint_as_float(ov[4 * y + 3]) * f);
@@ -734,28 +832,35 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
                 make_float4(m_run, none ? 0.f : l_run, bar->nan[slot] ? 1.f : 0.f, 0.f);
         } else {
           const long long orow = (long long)(it.q.tok0 + tok) * p.Hq + hq;
-          uint16_t* out = static_cast<uint16_t*>(p.o) + orow * D;
+          uint16_t* out = static_cast<uint16_t*>(p.o);
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t ov[32];
             tmem_ld32(tO + cc * 32, ov);
             tmem_ld_wait();
-            if (live) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint32_t pk[4];
+            for (int y = 0; y < 4; ++y) {
+              uint32_t pk[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const float a = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z]) * f;
-                  const float b = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z + 1]) * f;
-                  pk[z] = p.bf16 ? pack_bf16x2(a, b) : pack_half2(a, b);
-                }
-                *reinterpret_cast<uint4*>(out + cc * 32 + 8 * y) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              for (int z = 0; z < 4; ++z) {
+                const float a = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z]) * f;
+                const float b = none ? 0.f : __uint_as_float(ov[8 * y + 2 * z + 1]) * f;
+                pk[z] = p.bf16 ? pack_bf16x2(a, b) : pack_half2(a, b);
               }
+              *piece_of(row, cc * 4 + y) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
+          __syncwarp();
+          const long long at = live ? orow * D : -1;
+#pragma unroll 4
+          for (int c = 0; c < CH; ++c) {
+            const long long o = __shfl_sync(0xffffffffu, at, c * (32 / CH) + lane / CH);
+            const uint4 v = *piece_of((row & ~31) + c * (32 / CH) + lane / CH, lane % CH);
+            if (o >= 0) *reinterpret_cast<uint4*>(out + o + lane % CH * 8) = v;
+          }
+          __syncwarp();
           if (live && p.lse) p.lse[orow] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
-          if (live && bar->nan[slot]) restore_nan<D>(p, it, pos, out);  // rare
+          if (live && bar->nan[slot]) restore_nan(p, it, D, pos, out + orow * D, 0, D);  // rare
         }
         tc_fence_before();
       }

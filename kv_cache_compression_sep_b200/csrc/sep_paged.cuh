@@ -20,7 +20,7 @@ struct PagedAttnParams {
   const int32_t *table, *lens, *indptr;
   long long* base;  // [S + 1] first tile of each sequence (workspace)
   float* part;      // parts of row tiles that several warps share (workspace)
-  int* chunk_plan;    // kernel of chunks: items, parts per item, then first item of each sequence (workspace)
+  int* chunk_plan;    // kernel of chunks: kPlanInts of its CTAs, then first item of each sequence (workspace)
   float* chunk_part;  // parts of its items (workspace)
   unsigned* err;
   int T, S, Hq, Hkv, G, num_pages, max_pages, log_page, a, n, bf16, nwarps;
@@ -72,6 +72,16 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool on) {
+  // a size of 0 reads nothing and fills with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 constexpr uint32_t kNoRow = 0xffffffffu;
 
 // The exponent fields of a page's scales (powers of two, or 0 while the page holds only zeros), and the
@@ -93,30 +103,35 @@ __device__ __forceinline__ void store_out(const PagedAttnParams& p, long long at
 constexpr float kLn2 = 0.69314718055994531f;
 
 // ------------------------------------------------------------------ items of the chunk kernel
-// 256 rows of one sequence and KV head. With few items each is cut along its keys into parts, one per CTA,
-// that leave their results, maxima and sums for the join.
+// 256 rows of one sequence and KV head; its steps are window tiles of 128 keys and scan steps. Whole items
+// go to the CTAs in turn, the longest rows of a sequence first. Where that would leave CTAs idle for long,
+// the items' steps are laid end to end instead, kStartUnits before each for its start, and every CTA takes
+// an equal run of that line. Items that a boundary cuts leave results, maxima and sums of their parts for
+// the join.
 constexpr int kRowsPerItem = 256;
 constexpr int kScanStep = 1024;  // positions examined per refill of the list of kept keys
 constexpr int kChunkCtas = 148;
+constexpr int kStartUnits = 4;
+constexpr int kSnap = 2;       // no part has fewer steps: its boundary moves to the item's start or end
+// What the cuts have to save: one more start per CTA and the join. (us, cut against whole: 152 items of 64 steps
+// 206 / 342, 256 of 64 306 / 337, 64 of 16 50 / 62; 256 of 14 steps, which the rule leaves whole, 104 / 94.)
+constexpr int kCutUnits = 8;
+constexpr int kPlanInts = 2 * kChunkCtas;  // by CTA: item that it cuts first, number of parts (0: none)
+constexpr int kChunkParts = 2 * kChunkCtas;  // slots: 2 c + 1 the part of CTA c that starts an item, 2 c one that goes on
 struct Item {
   SeqInfo q;
   int seq, h, r0, rows;  // first row, rows of the sequence
   int w0, kend;          // window keys [w0, kend); listed keys left of w0
+  int steps;
   int scan0, scan1, win0, win1;  // this part's share of both
 };
 __device__ __forceinline__ int chunk_items(const PagedAttnParams& p, const SeqInfo& q) {
   if (!is_chunk(p, q)) return 0;
   return p.Hkv * (int)(((long long)q.nq * p.G + kRowsPerItem - 1) / kRowsPerItem);
 }
-// Steps (window tiles of 128 keys, scan steps) of a sequence's last item.
-__device__ __forceinline__ int chunk_steps(const PagedAttnParams& p, const SeqInfo& q) {
-  const int w0 = max(0, q.len - (q.nq < kRowsPerItem ? q.nq : kRowsPerItem) - max(p.n, 1) + 1) & ~127;
-  return (w0 + kScanStep - 1) / kScanStep + (q.len - w0 + 127) / 128;
-}
-// Part x % parts of item x / parts; within a sequence the latest (longest) rows first.
-__device__ __forceinline__ Item chunk_item(const PagedAttnParams& p, const int* base, int x, int parts) {
+// Steps [s0, min(s1, steps)) of an item.
+__device__ __forceinline__ Item chunk_item(const PagedAttnParams& p, const int* base, int item, int s0, int s1) {
   Item it;
-  const int item = x / parts, part = x - item * parts;
   int lo = 0, hi = p.S;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -134,81 +149,89 @@ __device__ __forceinline__ Item chunk_item(const PagedAttnParams& p, const int* 
   const int hi_pos = it.q.lead + min(it.q.nq - 1, (it.r0 + kRowsPerItem - 1) / p.G);
   it.kend = max(0, hi_pos + 1);
   it.w0 = min(max(0, lo_pos - max(p.n, 1) + 1), it.kend) & ~127;
-  const int ns = (it.w0 + kScanStep - 1) / kScanStep, steps = ns + (it.kend - it.w0 + 127) / 128;
-  const int a = (int)((long long)steps * part / parts), b = (int)((long long)steps * (part + 1) / parts);
-  it.scan0 = min(it.w0, a * kScanStep);
-  it.scan1 = min(it.w0, b * kScanStep);
+  const int ns = (it.w0 + kScanStep - 1) / kScanStep;
+  it.steps = ns + (it.kend - it.w0 + 127) / 128;
+  const int a = s0, b = min(s1, it.steps);
+  it.scan0 = min(it.w0, min(a, ns) * kScanStep);
+  it.scan1 = min(it.w0, min(b, ns) * kScanStep);
   it.win0 = min(it.kend, it.w0 + max(0, a - ns) * 128);
   it.win1 = min(it.kend, it.w0 + max(0, b - ns) * 128);
   return it;
 }
-// The output row's elements become NaN where a kept key's value is NaN (the products took those as 0).
-template <int D>
-__device__ __forceinline__ void restore_nan(const PagedAttnParams& p, const Item& it, int pos, uint16_t* out) {
+// Columns [c0, c1) of the output row become NaN where a kept key's value is NaN (the products took those
+// as 0).
+__device__ __forceinline__ void restore_nan(const PagedAttnParams& p, const Item& it, int d, int pos, uint16_t* out, int c0,
+                                         int c1) {
   const int32_t* table = p.table + (long long)it.seq * p.max_pages;
   for (int j = 0; j <= pos; ++j) {
     const int id = __ldg(table + (j >> p.log_page));
     if (id < 0 || id >= p.num_pages) continue;
     const int off = j & ((1 << p.log_page) - 1);
     if (!(pos - j < p.n || j < p.a || __ldg(p.flags + ((size_t)id << p.log_page) + off) != 0)) continue;
-    const uint8_t* v = p.v_pages + ((((size_t)id * p.Hkv + it.h) << p.log_page) + off) * D;
-    for (int c = 0; c < D / 4; ++c) {
-      const uint32_t b = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(v) + c));
+    const uint8_t* v = p.v_pages + ((((size_t)id * p.Hkv + it.h) << p.log_page) + off) * d;
+    for (int c = c0; c < c1; c += 4) {
+      const uint32_t b = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(v + c)));
       for (int y = 0; y < 4; ++y)
-        if (b >> (8 * y) & 0x80u) out[4 * c + y] = 0x7fffu;  // NaN in bf16 and fp16
+        if (b >> (8 * y) & 0x80u) out[c + y] = 0x7fffu;  // NaN in bf16 and fp16
     }
   }
 }
-// Part of an item in the workspace: [256][D] results, then [256][4] of maximum, sum, NaN flag.
+// Part of an item in the workspace: results by column group, [D / 4][256][4], then [256][4] of maximum, sum,
+// NaN flag. (One lane of the chunk kernel has one row: its 32 lanes' 16-byte stores are 512 bytes in a row.)
 template <int D>
-__device__ __forceinline__ float* chunk_part_of(const PagedAttnParams& p, int x) {
-  return p.chunk_part + (size_t)x * (kRowsPerItem * (D + 4));
+__device__ __forceinline__ float* chunk_part_of(const PagedAttnParams& p, int slot) {
+  return p.chunk_part + (size_t)slot * (kRowsPerItem * (D + 4));
 }
-// Row r of item `item`, by one warp.
+// Eight rows from r0 and 32 columns from col0 of an item that CTA c starts and the next ones go on with, by
+// one warp: eight columns of a row per lane.
 template <int D>
-__device__ __forceinline__ void chunk_join_row(const PagedAttnParams& p, int item, int r, int parts, int lane) {
-  constexpr int F = D / 32;  // columns per lane
-  const Item it = chunk_item(p, p.chunk_plan + 2, item * parts, parts);
+__device__ __forceinline__ void chunk_join_rows(const PagedAttnParams& p, const Item& it, int c, int parts, int r0, int col0,
+                                                int lane) {
+  const int r = r0 + (lane & 7), col = col0 + (lane >> 3) * 8;
   if (it.r0 + r >= it.rows) return;
   const int tok = (it.r0 + r) / p.G, hq = it.h * p.G + (it.r0 + r) - tok * p.G;
-  auto stats = [&](int i) {
-    return *reinterpret_cast<const float4*>(chunk_part_of<D>(p, item * parts + i) + kRowsPerItem * D + r * 4);
-  };
+  auto part = [&](int i) { return chunk_part_of<D>(p, 2 * (c + i) + (i == 0)); };
+  auto stats = [&](int i) { return *reinterpret_cast<const float4*>(part(i) + kRowsPerItem * D + r * 4); };
   float m = -INFINITY;
   bool bad = false;
+#pragma unroll 4
   for (int i = 0; i < parts; ++i) {
     const float4 st = stats(i);
     m = fmaxf(m, st.x);
     bad |= st.z != 0.f;
   }
   const float mr = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[F];
+  float l = 0.f, acc[8];
 #pragma unroll
-  for (int y = 0; y < F; ++y) acc[y] = 0.f;
+  for (int y = 0; y < 8; ++y) acc[y] = 0.f;
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
     const float4 st = stats(i);
     const float f = st.y * ex2(st.x - mr);  // the part's share of the sum
     l += f;
-    const float* a = chunk_part_of<D>(p, item * parts + i) + (size_t)r * D + lane * F;
+    const float* a = part(i) + ((col >> 2) * kRowsPerItem + r) * 4;
 #pragma unroll
-    for (int y = 0; y < F; y += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(a + y);
-      acc[y] = fmaf(v.x, f, acc[y]);
-      acc[y + 1] = fmaf(v.y, f, acc[y + 1]);
+    for (int y = 0; y < 2; ++y) {
+      const float4 v = *reinterpret_cast<const float4*>(a + y * kRowsPerItem * 4);
+      acc[4 * y] = fmaf(v.x, f, acc[4 * y]);
+      acc[4 * y + 1] = fmaf(v.y, f, acc[4 * y + 1]);
+      acc[4 * y + 2] = fmaf(v.z, f, acc[4 * y + 2]);
+      acc[4 * y + 3] = fmaf(v.w, f, acc[4 * y + 3]);
     }
   }
   const bool none = m == -INFINITY && !(l != l);
   const float f = none ? 0.f : 1.f / l;
   const long long row = (long long)(it.q.tok0 + tok) * p.Hq + hq;
+  uint32_t w[4];
 #pragma unroll
-  for (int y = 0; y < F; y += 2)
-    store_out(p, row * D + lane * F + y, none ? 0.f : acc[y] * f, none ? 0.f : acc[y + 1] * f);
-  if (lane == 0 && p.lse) p.lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-  if (bad) {
-    __syncwarp();
-    if (lane == 0) restore_nan<D>(p, it, it.q.lead + tok, static_cast<uint16_t*>(p.o) + row * D);
+  for (int y = 0; y < 4; ++y) {
+    const float a = none ? 0.f : acc[2 * y] * f, b = none ? 0.f : acc[2 * y + 1] * f;
+    w[y] = p.bf16 ? pack_bf16x2(a, b) : pack_half2(a, b);
   }
+  uint16_t* out = static_cast<uint16_t*>(p.o) + row * D;
+  *reinterpret_cast<uint4*>(out + col) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (col == 0 && p.lse) p.lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (bad) restore_nan(p, it, D, it.q.lead + tok, out, col, col + 8);
 }
 
 cudaError_t launch_paged_chunks(const PagedAttnParams& p, int d, cudaStream_t stream);
