@@ -295,6 +295,10 @@ ATTN = [
     ((300, 64, 5000), (1, 1, 1), 40, 1, 64, 16, "bfloat16", 0, None),  # single tokens of a wide group
     ((6000, 200), (40, 3), 1, 1, 128, 64, "bfloat16", 0, None),   # one item, cut along its keys
     ((6000, 200), (40, 3), 2, 1, 64, 32, "bfloat16", 4, 200),
+    # items shared by steps: just more than the SMs, fewer, few with parts of listed keys only
+    ((1300, 1250, 900), (256, 256, 256), 50, 50, 64, 64, "float16", 0, None),
+    ((1500, 1400), (300, 90), 32, 4, 128, 64, "bfloat16", 0, None),
+    ((9000, 40), (64, 2), 8, 2, 128, 16, "bfloat16", 4, 256),
 ]
 
 
@@ -399,6 +403,26 @@ def test_nan_reaches_only_the_rows_that_keep_it(S, what, c):
             else:
                 assert torch.isnan(o[i, hq, t[1]]) and torch.isnan(o[i, hq]).sum() == 1
                 assert torch.equal(lse[i, hq], clean_lse[i, hq])
+
+
+def test_nan_in_an_item_of_several_parts(S):
+    """A NaN value in a long sequence whose items are cut along their keys: one column of the rows that keep
+    the token, and nothing else, is NaN."""
+    import torch
+    L, c, n = 6000, 64, 1500
+    pair = filled(S, 1, (L,), 1, 128, 64, seed=3, p=0.0)
+    q = draw(4, c, 2, 128, torch.float16)
+    plan = (ints(pair.table.tolist()), ints([L]), ints([0, c]))
+    clean, clean_lse = pair.cache.seppaged_attn(q, *plan, n=n)
+    j = L - c - n + 30  # in the window of the first 30 queries
+    pair.cache.v_pages.view(torch.uint8)[int(pair.table[0][j // 64]), 0, j % 64, 77] = 0xFF
+    o, lse = pair.cache.seppaged_attn(q, *plan, n=n)
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0 and torch.equal(lse, clean_lse)
+    keeps = torch.arange(L - c, L, device="cuda") - j < n
+    assert 0 < int(keeps.sum()) < c
+    assert torch.equal(o[~keeps], clean[~keeps])
+    assert torch.isnan(o[keeps][:, :, 77]).all() and int(torch.isnan(o[keeps]).sum()) == 2 * int(keeps.sum())
 
 
 def test_chunk_with_pages_of_zeros_and_far_scales(S):
