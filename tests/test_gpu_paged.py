@@ -405,6 +405,26 @@ def test_nan_reaches_only_the_rows_that_keep_it(S, what, c):
                 assert torch.equal(lse[i, hq], clean_lse[i, hq])
 
 
+@pytest.mark.parametrize("seqs,first,c,Hq", [(501, 20000, 33, 1),   # one long item among many short ones
+                                             (4096, 90, 17, 2)])    # as many sequences as a call takes
+def test_many_chunks(S, seqs, first, c, Hq):
+    import torch
+    lens, counts = [first] + [60 + i % 40 for i in range(seqs - 1)], [c] * seqs
+    page, long = 64, -(-first // 64)
+    cache = S.SepPagedCache(long + 2 * seqs, 1, 64, page=page)
+    table = np.full((seqs, max(long, 2)), -1)
+    table[0, :long] = np.arange(long)
+    table[1:, :2] = long + np.arange(2 * (seqs - 1)).reshape(-1, 2)
+    k, v = (draw(s, sum(lens), 1, 64, torch.bfloat16, 1) for s in (1, 2))
+    cache.seppaged_append(k, v, ints(table.tolist()), ints(lens), ints(np.concatenate([[0], np.cumsum(lens)]).tolist()))
+    q = draw(3, sum(counts), Hq, 64, torch.bfloat16, 1)
+    o, lse = cache.seppaged_attn(q, ints(table.tolist()), ints(lens), ints((c * np.arange(seqs + 1)).tolist()))
+    torch.cuda.synchronize()
+    assert S.sep_last_device_error() == 0
+    pair = type("", (), dict(cache=cache, table=table, lens=lens))
+    check_attn(pair, q, o, lse, counts, 0, None, 0.125, only={0, 1, 2, 147, 148, 300, 416, 417, seqs - 2, seqs - 1})
+
+
 def test_nan_in_an_item_of_several_parts(S):
     """A NaN value in a long sequence whose items are cut along their keys: one column of the rows that keep
     the token, and nothing else, is NaN."""
