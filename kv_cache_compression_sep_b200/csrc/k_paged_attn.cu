@@ -996,9 +996,8 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_const
   constexpr int R = 8 * NT;
   const int lane = threadIdx.x & 31, x = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int tok = x / p.Hq, hq = x - tok * p.Hq;
-  grid_dep_wait();
-  grid_dep_launch_next();
-  if (tok >= p.T) return;
+  // The call's arguments are read ahead of the wait: they were there before the kernel that this one waits for
+  // passed its own wait and let this one start.
   // sequence of the token: last s with indptr[s] <= tok
   int seq = -1;
   for (int s0 = 0; s0 < p.S; s0 += 32) {
@@ -1006,12 +1005,13 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const __grid_const
     seq += hit;
     if (hit < min(32, p.S - s0)) break;
   }
-  if (seq < 0) return;
-  const long long base = p.base[seq], total = p.base[p.S];
-  const SeqInfo q = seq_info(p, seq);
-  if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
+  const SeqInfo q = seq_info(p, max(seq, 0));
   const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
   const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+  grid_dep_wait();
+  grid_dep_launch_next();
+  if (tok >= p.T || seq < 0 || tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
+  const long long base = p.base[seq], total = p.base[p.S];
   const long long t0 = base + ((long long)h * nrt + row / R) * per_rt;
   join_row_warp<D, NT>(p, q, h, row, t0, t0 + per_rt, Split(total, p.nwarps));
 }
@@ -1022,10 +1022,10 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int R = 8 * NT;
   __shared__ JoinShared<D> sh;
-  grid_dep_wait();
-  grid_dep_launch_next();
   const int tid = threadIdx.x;
   if (p.chunks) {
+    grid_dep_wait();
+    grid_dep_launch_next();
     // a CTA per 32 rows of an item that was cut
     constexpr int PER = kRowsPerItem / 32;
     for (int x = blockIdx.x; x < kChunkCtas * PER; x += gridDim.x) {
@@ -1064,11 +1064,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     seq += hit;
     if (hit < min(kJoinThreads, p.S - s0)) break;
   }
-  if (seq < 0) return;
-  const SeqInfo q = seq_info(p, seq);
-  if (tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
+  const SeqInfo q = seq_info(p, max(seq, 0));
   const int h = hq / p.G, row = (tok - q.tok0) * p.G + (hq - h * p.G);
   const int per_rt = tiles_per_row_tile(p, q, R), nrt = row_tiles(p, q, R);
+  grid_dep_wait();  // (what is above reads the call's arguments only)
+  grid_dep_launch_next();
+  if (seq < 0 || tok < q.tok0 || tok >= q.tok0 + q.nq || q.len == 0) return;
   const long long t0 = p.base[seq] + ((long long)h * nrt + row / R) * per_rt;
   join_row<D, NT>(p, sh, q, h, row, t0, t0 + per_rt, Split(p.base[p.S], p.nwarps));
 }
