@@ -769,23 +769,26 @@ class SepPagedCache:
                              (r.freq.data_ptr(), r.d_rot, r.interleaved, r.magnitude)))
 
     def _state(self):
-        """Checks the cache's own tensors where a caller has put its own buffers in their place."""
-        seen = self._seen
-        if (seen is not None and self.k_pages is seen[0] and self.v_pages is seen[1] and
-                self.k_scale is seen[2] and self.v_scale is seen[3] and self.flags is seen[4]):
-            return
+        """Checks the cache's own tensors: a caller may have put others, or other storage, in their
+        place."""
+        k, v, ks, vs, fl = self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.flags
         pages, per_head = (self.num_pages, self.Hkv, self.page, self.d), (self.num_pages, self.Hkv)
-        for name, t, dtype, shape in (("k_pages", self.k_pages, torch.float8_e4m3fn, pages),
-                                      ("v_pages", self.v_pages, torch.float8_e4m3fn, pages),
-                                      ("k_scale", self.k_scale, torch.float32, per_head),
-                                      ("v_scale", self.v_scale, torch.float32, per_head),
-                                      ("flags", self.flags, torch.uint8, pages[::2])):
-            if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or \
-                    not t.is_contiguous() or not t.is_cuda:
-                _cuda(t, dtype, name, shape)
-        self._seen = (self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.flags)
-
-    _seen = None
+        slots, e4m3, f32 = (self.num_pages, self.page), torch.float8_e4m3fn, torch.float32
+        try:
+            if (k.shape == pages and v.shape == pages and ks.shape == per_head and
+                    vs.shape == per_head and fl.shape == slots and
+                    k.dtype is e4m3 and v.dtype is e4m3 and ks.dtype is f32 and vs.dtype is f32 and
+                    fl.dtype is torch.uint8 and k.is_contiguous() and v.is_contiguous() and
+                    ks.is_contiguous() and vs.is_contiguous() and fl.is_contiguous() and
+                    k.is_cuda):  # (one device for all: checked with the other tensors)
+                return
+        except AttributeError:
+            pass
+        for name, t, dtype, shape in (("k_pages", k, e4m3, pages), ("v_pages", v, e4m3, pages),
+                                      ("k_scale", ks, f32, per_head),
+                                      ("v_scale", vs, f32, per_head),
+                                      ("flags", fl, torch.uint8, slots)):
+            _cuda(t, dtype, name, shape)
 
     @staticmethod
     def _plan(page_table, seq_lens, indptr):

@@ -175,6 +175,20 @@ def test_paged_constructor_refusals():
             S.SepPagedCache(**args)
 
 
+@pytest.mark.parametrize("name", ["k_pages", "v_pages", "k_scale", "v_scale", "flags"])
+def test_state_of_another_size_is_refused(monkeypatch, name):
+    """Also when the tensor object is the one that an earlier call accepted."""
+    c = _paged(monkeypatch)
+    c._state()
+    t = getattr(c, name)
+    t.resize_(t.shape[0] - 1, *t.shape[1:])
+    with pytest.raises(S.SepError, match=name):
+        c._state()
+    setattr(c, name, None)
+    with pytest.raises(S.SepError, match=name):
+        c._state()
+
+
 def test_append_binding_refusals(monkeypatch):
     c = _paged(monkeypatch)
     k = FakeCuda(torch.zeros(3, 2, 64, dtype=torch.bfloat16))
