@@ -77,7 +77,8 @@ struct ChunkBar {
   int ex_k[4], ex_v[4], nan[4];
   int red[4], part4[4], any_far[2][4], hole[2][4];
   int part[16];
-  long long sum[16], sum0[16];
+  long long sum[16];
+  unsigned load[kChunkCtas];  // units of each CTA if it takes every 148th item whole
   int cut_item[2], cut_step[2], cut_last;  // ends of the CTA's run; last CTA with a part of the item at its end
   uint32_t tmem_base;
   int abort_flag;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
   grid_dep_launch_next();
   // ---- first item of every sequence
   int carry = 0;
+  if (tid < kChunkCtas) bar->load[tid] = 0;
   __syncthreads();
   for (int s0 = 0; s0 < p.S; s0 += C::THREADS) {
     const int s = s0 + tid;
@@ -215,30 +217,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::THREADS, 1) paged_chunk_kernel(co
   // ---- this CTA's items first + i stride, from step step0 of the first to step1 of the last
   const int cta = blockIdx.x, tiles = carry / p.Hkv;
   auto units_of = [&](int f) { return chunk_item(p, base, f * p.Hkv, 0, 0).steps + kStartUnits; };
-  long long total = 0, load0 = 0;  // units; those of CTA 0 if it takes every 148th item whole
+  long long total = 0;  // units
   int units0 = 0;
   for (int f = tid; f < tiles; f += C::THREADS) {
     const int v = units_of(f);
     if (f == tid) units0 = v;
     total += (long long)v * p.Hkv;
-    load0 += (long long)v * (((f + 1) * p.Hkv + kChunkCtas - 1) / kChunkCtas - (f * p.Hkv + kChunkCtas - 1) / kChunkCtas);
+    for (int h = 0, c = f * p.Hkv % kChunkCtas; h < p.Hkv; ++h, c = c + 1 == kChunkCtas ? 0 : c + 1)
+      atomicAdd(&bar->load[c], (unsigned)v);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    load0 += __shfl_xor_sync(0xffffffffu, load0, o);
-  }
-  if (lane == 0) {
-    bar->sum[warp] = total;
-    bar->sum0[warp] = load0;
-  }
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) bar->sum[warp] = total;
   __syncthreads();
-  total = load0 = 0;
-  for (int w = 0; w < C::THREADS / 32; ++w) {
-    total += bar->sum[w];
-    load0 += bar->sum0[w];
-  }
-  const bool cut = (load0 - kCutUnits) * kChunkCtas > total;
+  total = 0;
+  for (int w = 0; w < C::THREADS / 32; ++w) total += bar->sum[w];
+  unsigned most = 0;
+  for (int c = lane; c < kChunkCtas; c += 32) most = max(most, bar->load[c]);
+  most = __reduce_max_sync(0xffffffffu, most);
+  const bool cut = ((long long)most - kCutUnits) * kChunkCtas > total;
   int first = cta, stride = kChunkCtas, nitems = carry > cta ? (carry - cta - 1) / kChunkCtas + 1 : 0;
   int step0 = 0, step1 = INT_MAX, parts = 0;
   if (cut) {

@@ -104,17 +104,18 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // ------------------------------------------------------------------ items of the chunk kernel
 // 256 rows of one sequence and KV head; its steps are window tiles of 128 keys and scan steps. Whole items
-// go to the CTAs in turn, the longest rows of a sequence first. Where that would leave CTAs idle for long,
-// the items' steps are laid end to end instead, kStartUnits before each for its start, and every CTA takes
-// an equal run of that line. Items that a boundary cuts leave results, maxima and sums of their parts for
-// the join.
+// go to the CTAs in turn, the longest rows of a sequence first. Where the busiest CTA would then have more
+// than the mean by kCutUnits, the items' steps are laid end to end instead, kStartUnits before each for its
+// start, and every CTA takes an equal run of that line. Items that a boundary cuts leave results, maxima and
+// sums of their parts for the join.
 constexpr int kRowsPerItem = 256;
 constexpr int kScanStep = 1024;  // positions examined per refill of the list of kept keys
 constexpr int kChunkCtas = 148;
 constexpr int kStartUnits = 4;
 constexpr int kSnap = 2;       // no part has fewer steps: its boundary moves to the item's start or end
-// What the cuts have to save: one more start per CTA and the join. (us, cut against whole: 152 items of 64 steps
-// 206 / 342, 256 of 64 306 / 337, 64 of 16 50 / 62; 256 of 14 steps, which the rule leaves whole, 104 / 94.)
+// What the cuts have to save: one more start per CTA and the join. (us, cut against whole: 152 items of 64
+// steps 206 / 342, 256 of 64 305 / 337, 64 of 16 50 / 62, 8 of 256 behind 8 of one 81 / 703; 256 of 14 steps, which
+// the rule leaves whole, 104 / 94.)
 constexpr int kCutUnits = 8;
 constexpr int kPlanInts = 2 * kChunkCtas;  // by CTA: item that it cuts first, number of parts (0: none)
 constexpr int kChunkParts = 2 * kChunkCtas;  // slots: 2 c + 1 the part of CTA c that starts an item, 2 c one that goes on

@@ -299,6 +299,7 @@ ATTN = [
     ((1300, 1250, 900), (256, 256, 256), 50, 50, 64, 64, "float16", 0, None),
     ((1500, 1400), (300, 90), 32, 4, 128, 64, "bfloat16", 0, None),
     ((9000, 40), (64, 2), 8, 2, 128, 16, "bfloat16", 4, 256),
+    ((50, 7000), (40, 64), 4, 2, 64, 64, "float16", 0, None),     # a short one in front
 ]
 
 
