@@ -15,7 +15,7 @@
 // between two e4m3 numbers may go to either, one in 10^5 does not go where the exact rotation would. Finding
 // them (both ends of the interval converted) takes 8 prompts of 8192 tokens from 67 to 106 us, deciding them
 // in fp64 to 146 us; against the half step that every key is rounded by it changes nothing. Every path turns alike,
-// so a key has the same bits whether it comes with a prompt or alone.
+// so the number that is rounded is the same whether a key comes with a prompt or alone.
 //
 // Two kernels. Pages that receive many rows (prompts): a CTA per (page, group of heads) holds a head's
 // rows in registers from the load over the maximum to the store, so each is read and written once;
